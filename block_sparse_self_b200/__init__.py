@@ -73,6 +73,21 @@ def lib() -> ctypes.CDLL:
         "vsa_centroid_compensated_attention": ([P, P, P, P, I, I, I, I, I, I, P, P, I, I, F, P, SZ, P], I),
         "vsa_centroid_compensated_attention_tiled": ([P, P, P, P, I, I, I, I, I, D3, P, I, P, P, P, I, I, F, P, SZ, P],
                                                      I),
+        "vsa_block_sparse_attention_lse": ([P, P, P, P, I, P, I, I, I, I, I, P, P, I, I, I, F, P], I),
+        "vsa_block_sparse_attention_tiled_lse": ([P, P, P, P, I, P, I, I, I, I, D3, P, I, P, P, P, I, I, I, F, P], I),
+        "vsa_window_attention_lse_workspace_size": ([I, I, I, I], SZ),
+        "vsa_window_attention_lse": ([P, P, P, P, I, P, I, I, I, I, I, I, F, P, I, I, I, P, SZ, P], I),
+        "vsa_block_sparse_attention_backward_workspace_size": ([I, I, I, I, I, I], SZ),
+        "vsa_block_sparse_attention_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, P, P, I, I, I, F, P,
+                                                 SZ, P], I),
+        "vsa_block_sparse_attention_tiled_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, D3, P, I, P, P, P,
+                                                       I, I, I, F, P, SZ, P], I),
+        "vsa_window_attention_backward_workspace_size": ([I, I, I, I, I], SZ),
+        "vsa_window_attention_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, F, P, I, I, I, P, P, SZ,
+                                           P], I),
+        "vsa_relative_position_buckets": ([I, I, P, P], I),
+        "vsa_transpose_block_lists_workspace_size": ([I, I], SZ),
+        "vsa_transpose_block_lists": ([P, P, I, I, I, P, P, P, SZ, P], I),
         "vsa_spade_attention_host_workspace_size": ([I, I, I, I, D3, P, I, I, I, I, I, I], SZ),
         "vsa_spade_attention_host": ([P, P, P, P, I, I, I, I, I, D3, P, I, I, I, I, F, I, P, SZ, P], I),
         "vsa_cast_f32_to_bf16": ([P, P, I64, P], I),
@@ -199,6 +214,26 @@ def select_tiling_noalloc(q: torch.Tensor, grid, tiles, return_sics: bool = Fals
     return (choice, sics) if return_sics else choice
 
 
+def _wants_grad(*tensors) -> bool:
+    """Whether a call over these tensors is to be recorded for a backward pass."""
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
+class _Permute(torch.autograd.Function):
+    """permute and unpermute: each one's gradient is the other."""
+
+    @staticmethod
+    def forward(ctx, x, grid, tiles, choice, inverse):
+        ctx.args, ctx.inverse = (grid, tiles), inverse
+        ctx.save_for_backward(choice)
+        return _permute(x, grid, tiles, choice, inverse)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        return _permute(g.contiguous(), *ctx.args, ctx.saved_tensors[0], not ctx.inverse), None, None, None, None
+
+
 def _permute(x, grid, tiles, choice, inverse):
     _cuda(x, "x")
     B, H, rows, D = _bhsd(x, "x")
@@ -221,12 +256,16 @@ def _permute(x, grid, tiles, choice, inverse):
 def permute(x: torch.Tensor, grid, tiles, choice: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Tile-contiguous order: y[b, h, p] = x[b, h, perm_c(p)] (c = choice[b*H+h] or 0).
     On a grid the tiles do not divide, y covers padded_grid(grid, tiles), with
-    zero rows at padding positions."""
+    zero rows at padding positions.  Differentiable in x."""
+    if _wants_grad(x):
+        return _Permute.apply(x, grid, tiles, choice, False)
     return _permute(x, grid, tiles, choice, False)
 
 
 def unpermute(y: torch.Tensor, grid, tiles, choice: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Inverse of permute: back to T-major order (padding rows dropped)."""
+    """Inverse of permute: back to T-major order (padding rows dropped).  Differentiable in y."""
+    if _wants_grad(y):
+        return _Permute.apply(y, grid, tiles, choice, True)
     return _permute(y, grid, tiles, choice, True)
 
 
@@ -429,27 +468,160 @@ def _out_dtype(out_dtype, ref):
     return dt
 
 
-def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, scale: Optional[float] = None,
-                           out_dtype=None) -> torch.Tensor:
-    """Softmax attention of each query block over the key blocks its list names (tile-contiguous order)."""
+def _qkv_shape(q, k, v):
     B, H, S, D = _bhsd(q, "q")
     if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
         raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
                          f"v={tuple(v.shape)}")
-    odt = _out_dtype(out_dtype, q)
-    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+    return B, H, S, D
+
+
+def _lists_arg(idx, cnt):
     _cuda(idx, "idx")
     _cuda(cnt, "cnt")
     if idx.dtype != torch.int32 or cnt.dtype != torch.int32:
         raise ValueError("idx and cnt must be int32")
+
+
+def _check_lists(idx, cnt, B, H, nb):
+    """The shapes that the training calls rely on: [B, H, nb, cap] and [B, H, nb], or [nb, cap] and [nb]."""
+    _lists_arg(idx, cnt)
+    want = (B, H, nb) if idx.dim() == 4 else (nb,)
+    if tuple(idx.shape[:-1]) != want or tuple(cnt.shape) != want:
+        raise ValueError(f"idx and cnt must be [B, H, nb, cap] and [B, H, nb], or [nb, cap] and [nb], with nb = {nb}; "
+                         f"got {tuple(idx.shape)} and {tuple(cnt.shape)}")
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, q on {ref.device}")
+
+
+def _code(dtype) -> int:
+    return BF16 if dtype == torch.bfloat16 else F32
+
+
+def _scale(scale) -> float:
+    return 0.0 if scale is None else float(scale)
+
+
+def _check_saved(do, q, o, lse):
+    """The forward pass's output and the gradient that comes back for it."""
+    B, H, S, D = q.shape
+    if tuple(do.shape) != (B, H, S, D) or tuple(o.shape) != (B, H, S, D):
+        raise ValueError(f"do and o must have q's shape {(B, H, S, D)}; got {tuple(do.shape)} and {tuple(o.shape)}")
+    _cuda(o, "o")
+    _dtype_code(o, "o")
+    _cuda(lse, "lse")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, S):
+        raise ValueError(f"lse must be float32 of shape {(B, H, S)}, as the forward call returns it")
+
+
+class _BlockSparse(torch.autograd.Function):
+    """block_sparse_attention and its tiled form: `kind` holds the two calls and their arguments."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, fwd, bwd, args, kw, out_dtype):
+        qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+        o, lse = fwd(qb, kb, vb, *args, out_dtype=_out_dtype(out_dtype, q), return_lse=True, **kw)
+        tensors = [a for a in args if isinstance(a, torch.Tensor)]
+        ctx.where = [isinstance(a, torch.Tensor) for a in args]
+        ctx.rest = [a for a in args if not isinstance(a, torch.Tensor)]
+        ctx.bwd, ctx.kw, ctx.dtypes = bwd, kw, (q.dtype, k.dtype, v.dtype)
+        ctx.save_for_backward(qb, kb, vb, o, lse, *tensors)
+        ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, _):
+        if do is None:
+            return (None,) * 8
+        qb, kb, vb, o, lse, *tensors = ctx.saved_tensors
+        tensors, rest = iter(tensors), iter(ctx.rest)
+        args = [next(tensors) if t else next(rest) for t in ctx.where]
+        f32 = any(t == torch.float32 for t in ctx.dtypes)
+        grads = ctx.bwd(do.contiguous(), qb, kb, vb, o, lse, *args, grad_dtype=torch.float32 if f32 else torch.bfloat16,
+                        **ctx.kw)
+        return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (None,) * 5
+
+
+def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, scale: Optional[float] = None,
+                           out_dtype=None, return_lse: bool = False):
+    """Softmax attention of each query block over the key blocks its list names (tile-contiguous order).
+
+    return_lse=True also returns the natural log of each row's softmax sum
+    (fp32 [B, H, S]), which block_sparse_attention_backward takes.
+    Differentiable in q, k and v; the lists are constants of the backward pass."""
+    if _wants_grad(q, k, v):
+        o, lse = _BlockSparse.apply(q, k, v, block_sparse_attention, block_sparse_attention_backward,
+                                    (idx, cnt, block), dict(group_size=group_size, scale=scale), out_dtype)
+        return (o, lse) if return_lse else o
+    B, H, S, D = _qkv_shape(q, k, v)
+    odt = _out_dtype(out_dtype, q)
+    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+    _lists_arg(idx, cnt)
     per_head = idx.dim() == 4
     cap = idx.shape[-1]
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    _check(lib().vsa_block_sparse_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), BF16 if odt == torch.bfloat16
-                                            else F32, B, H, S, D, int(block), _ptr(idx), _ptr(cnt), int(cap),
-                                            1 if per_head else 0, int(group_size),
-                                            0.0 if scale is None else float(scale), _stream(q.device)))
+    if return_lse:
+        lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device)
+        _check(lib().vsa_block_sparse_attention_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), B, H,
+                                                    S, D, int(block), _ptr(idx), _ptr(cnt), int(cap),
+                                                    1 if per_head else 0, int(group_size), _scale(scale),
+                                                    _stream(q.device)))
+        return o, lse
+    _check(lib().vsa_block_sparse_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(block),
+                                            _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size),
+                                            _scale(scale), _stream(q.device)))
     return o
+
+
+def block_sparse_attention_backward(do, q, k, v, o, lse, idx, cnt, block: int, group_size: int = 0,
+                                    scale: Optional[float] = None, grad_dtype=None):
+    """(dq, dk, dv) of block_sparse_attention for the gradient `do` of its output, from that output
+    and its lse.  The gradients have q's type unless grad_dtype says otherwise."""
+    B, H, S, D = _qkv_shape(q, k, v)
+    gdt = _out_dtype(grad_dtype, q)
+    _check_saved(do, q, o, lse)
+    qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
+    if block not in (32, 64, 128) or S % block:
+        raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
+    _check_lists(idx, cnt, B, H, S // block)
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, idx=idx, cnt=cnt)
+    cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
+    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
+    with torch.cuda.device(q.device):
+        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, S, int(block), cap, per_head)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _check(lib().vsa_block_sparse_attention_backward(
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _code(gdt), B, H, S, D, int(block), _ptr(idx), _ptr(cnt), cap, per_head, int(group_size), _scale(scale),
+            _ptr(ws), need, _stream(q.device)))
+    return dq, dk, dv
+
+
+def transpose_block_lists(idx, cnt):
+    """Block lists turned round: (offsets [..., nb + 1], rows [..., nb * cap]), int32.  Key block j is
+    listed by the query blocks rows[..., offsets[j]:offsets[j + 1]], ascending; rows holds -1 behind
+    the last entry.  idx [..., nb, cap] and cnt [..., nb] as the list calls return them."""
+    _lists_arg(idx, cnt)
+    if idx.dim() < 2 or idx.shape[:-1] != cnt.shape or idx.numel() == 0:
+        raise ValueError(f"idx must be [..., nb, cap] and cnt [..., nb]; got {tuple(idx.shape)} and {tuple(cnt.shape)}")
+    if cnt.device != idx.device:
+        raise ValueError(f"cnt is on {cnt.device}, idx on {idx.device}")
+    lead, (nb, cap) = idx.shape[:-2], idx.shape[-2:]
+    lists = math.prod(lead)
+    offsets = torch.empty(*lead, nb + 1, dtype=torch.int32, device=idx.device)
+    rows = torch.empty(*lead, nb * cap, dtype=torch.int32, device=idx.device)
+    with torch.cuda.device(idx.device):
+        need = lib().vsa_transpose_block_lists_workspace_size(lists, nb)
+        ws = torch.empty(need, dtype=torch.uint8, device=idx.device)
+        _check(lib().vsa_transpose_block_lists(_ptr(idx), _ptr(cnt), lists, nb, cap, _ptr(offsets), _ptr(rows),
+                                               _ptr(ws), need, _stream(idx.device)))
+    return offsets, rows
 
 
 def centroid_compensated_attention(q, k, v, idx, cnt, block: int = 128, scale: Optional[float] = None,
@@ -510,29 +682,60 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
 
 
 def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: Optional[float] = None,
-                                 out_dtype=None, group_stride: int = 0) -> torch.Tensor:
+                                 out_dtype=None, group_stride: int = 0, return_lse: bool = False):
     """unpermute(block_sparse_attention(permute(q), permute(k), permute(v), idx, cnt, block)) in one
     kernel: q, k, v and the result stay in T-major order; lists number the blocks of each
     head's tile-contiguous order (block = the tile volume if 32 or 64, else 128 tokens).
     group_stride s > 0 (128-token blocks) restricts each query to keys whose position
-    differs from its own by a multiple of s (see include/vsa.h)."""
-    B, H, S, D = _bhsd(q, "q")
-    if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
-        raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
-                         f"v={tuple(v.shape)}")
+    differs from its own by a multiple of s (see include/vsa.h).  return_lse and
+    differentiability as for block_sparse_attention; lse is in T-major order."""
+    if _wants_grad(q, k, v):
+        o, lse = _BlockSparse.apply(q, k, v, block_sparse_attention_tiled, block_sparse_attention_tiled_backward,
+                                    (grid, tiles, choice, idx, cnt), dict(scale=scale, group_stride=group_stride),
+                                    out_dtype)
+        return (o, lse) if return_lse else o
+    B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-    _cuda(idx, "idx")
-    _cuda(cnt, "cnt")
-    if idx.dtype != torch.int32 or cnt.dtype != torch.int32:
-        raise ValueError("idx and cnt must be int32")
+    _lists_arg(idx, cnt)
     arr, n = _tiles_arg(tiles)
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    _check(lib().vsa_block_sparse_attention_tiled(
-        _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), BF16 if odt == torch.bfloat16 else F32, B, H, S, D, Dims3(*grid),
-        arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), int(idx.shape[-1]), 1 if idx.dim() == 4 else 0,
-        int(group_stride), 0.0 if scale is None else float(scale), _stream(q.device)))
+    tail = (B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), int(idx.shape[-1]),
+            1 if idx.dim() == 4 else 0, int(group_stride), _scale(scale), _stream(q.device))
+    if return_lse:
+        lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device)
+        _check(lib().vsa_block_sparse_attention_tiled_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse),
+                                                          *tail))
+        return o, lse
+    _check(lib().vsa_block_sparse_attention_tiled(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), *tail))
     return o
+
+
+def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choice, idx, cnt,
+                                          scale: Optional[float] = None, group_stride: int = 0, grad_dtype=None):
+    """(dq, dk, dv) of block_sparse_attention_tiled, all in T-major order, for the gradient `do` of its
+    output, from that output and its lse.  The gradients have q's type unless grad_dtype says otherwise."""
+    B, H, S, D = _qkv_shape(q, k, v)
+    gdt = _out_dtype(grad_dtype, q)
+    _check_saved(do, q, o, lse)
+    qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
+    arr, n = _tiles_arg(tiles)
+    positions = _grid_tokens(padded_grid(grid, tiles))
+    block = min(128, math.prod(int(x) for x in tiles[0]))
+    if block not in (32, 64, 128) or positions % block:
+        raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {math.prod(tiles[0])}")
+    _check_lists(idx, cnt, B, H, positions // block)
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, idx=idx, cnt=cnt, choice=choice)
+    cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
+    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
+    with torch.cuda.device(q.device):
+        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, positions, block, cap, per_head)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _check(lib().vsa_block_sparse_attention_tiled_backward(
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _code(gdt), B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), cap,
+            per_head, int(group_stride), _scale(scale), _ptr(ws), need, _stream(q.device)))
+    return dq, dk, dv
 
 
 def tiled_supported(tiles) -> bool:
@@ -549,22 +752,115 @@ def tiled_supported(tiles) -> bool:
     return vol % 128 == 0 and all(t[0] % (vol // 128) == 0 for t in tiles)
 
 
+def _bias_arg(bias, H):
+    """A relative position bias [num_buckets, H]: its number of buckets."""
+    _cuda(bias, "bias")
+    _dtype_code(bias, "bias")
+    if bias.dim() != 2 or bias.shape[1] != H:
+        raise ValueError(f"bias must be [num_buckets, {H}] (buckets by heads), got {tuple(bias.shape)}")
+    return int(bias.shape[0])
+
+
+class _Window(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, bias, window, kw, out_dtype):
+        qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+        o, lse = window_attention(qb, kb, vb, window, out_dtype=_out_dtype(out_dtype, q), bias=bias, return_lse=True,
+                                  **kw)
+        ctx.window, ctx.kw, ctx.dtypes = window, kw, (q.dtype, k.dtype, v.dtype)
+        ctx.save_for_backward(qb, kb, vb, o, lse, bias)
+        ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, _):
+        if do is None:
+            return (None,) * 7
+        qb, kb, vb, o, lse, bias = ctx.saved_tensors
+        f32 = any(t == torch.float32 for t in ctx.dtypes)
+        kw = {n: x for n, x in ctx.kw.items() if n != "chunk_size"}
+        grads = window_attention_backward(do.contiguous(), qb, kb, vb, o, lse, ctx.window, bias=bias,
+                                          grad_dtype=torch.float32 if f32 else torch.bfloat16,
+                                          bias_grad=ctx.needs_input_grad[3], **kw)
+        dbias = grads[3] if ctx.needs_input_grad[3] else None
+        return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (dbias, None, None, None)
+
+
 def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float] = None,
-                     chunk_size: Optional[int] = None, out_dtype=None) -> torch.Tensor:
-    """Symmetric sliding-window attention with `sink` global keys (dense when window >= S)."""
-    B, H, S, D = _bhsd(q, "q")
-    if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
-        raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
-                         f"v={tuple(v.shape)}")
+                     chunk_size: Optional[int] = None, out_dtype=None, bias: Optional[torch.Tensor] = None,
+                     max_distance: int = 128, return_lse: bool = False):
+    """Symmetric sliding-window attention with `sink` global keys (dense when window >= S).
+
+    bias ([num_buckets, H], float32 or bfloat16) is a learned relative position
+    bias: bias[bucket(j - i), h] is added to the scaled logit of query i and key
+    j of head h, with the buckets of relative_position_buckets(num_buckets,
+    max_distance).  return_lse=True also returns the natural log of each row's
+    softmax sum (fp32 [B, H, S]), which window_attention_backward takes.
+    Differentiable in q, k, v and bias."""
+    if _wants_grad(q, k, v, bias):
+        kw = dict(sink=sink, scale=scale, chunk_size=chunk_size, max_distance=max_distance)
+        o, lse = _Window.apply(q, k, v, bias, window, kw, out_dtype)
+        return (o, lse) if return_lse else o
+    B, H, S, D = _qkv_shape(q, k, v)
     if chunk_size is not None and int(chunk_size) < 1:
         raise ValueError(f"chunk_size must be >= 1, got {chunk_size}")
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    _check(lib().vsa_window_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), BF16 if odt == torch.bfloat16 else F32,
-                                      B, H, S, D, int(window), int(sink), 0.0 if scale is None else float(scale),
-                                      0 if chunk_size is None else int(chunk_size), _stream(q.device)))
-    return o
+    if bias is None and not return_lse:
+        _check(lib().vsa_window_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(window),
+                                          int(sink), _scale(scale), 0 if chunk_size is None else int(chunk_size),
+                                          _stream(q.device)))
+        return o
+    lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device) if return_lse else None
+    buckets, need, ws = 0, 0, None
+    _same_device(q, k=k, v=v, bias=bias)
+    with torch.cuda.device(q.device):
+        if bias is not None:
+            buckets = _bias_arg(bias, H)
+            need = lib().vsa_window_attention_lse_workspace_size(H, S, buckets, int(max_distance))
+            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        _check(lib().vsa_window_attention_lse(
+            _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), B, H, S, D, int(window), int(sink),
+            _scale(scale), _ptr(bias), F32 if bias is None else _code(bias.dtype), buckets, int(max_distance),
+            _ptr(ws), need, _stream(q.device)))
+    return (o, lse) if return_lse else o
+
+
+def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, scale: Optional[float] = None,
+                              bias: Optional[torch.Tensor] = None, max_distance: int = 128, grad_dtype=None,
+                              bias_grad: bool = True):
+    """(dq, dk, dv) of window_attention for the gradient `do` of its output, from that output and its
+    lse; with a bias (dq, dk, dv, dbias), dbias in the bias's type, or None with bias_grad=False.
+    The gradients of q, k and v have q's type unless grad_dtype says otherwise."""
+    B, H, S, D = _qkv_shape(q, k, v)
+    gdt = _out_dtype(grad_dtype, q)
+    _check_saved(do, q, o, lse)
+    qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, bias=bias)
+    buckets = 0 if bias is None else _bias_arg(bias, H)
+    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
+    dbias = None if bias is None or not bias_grad else torch.empty_like(bias)
+    with torch.cuda.device(q.device):
+        need = lib().vsa_window_attention_backward_workspace_size(B, H, S, buckets, int(max_distance))
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        _check(lib().vsa_window_attention_backward(
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _code(gdt), B, H, S, D, int(window), int(sink), _scale(scale), _ptr(bias),
+            F32 if bias is None else _code(bias.dtype), buckets, int(max_distance), _ptr(dbias), _ptr(ws), need,
+            _stream(q.device)))
+    return (dq, dk, dv) if bias is None else (dq, dk, dv, dbias)
+
+
+def relative_position_buckets(num_buckets: int, max_distance: int, device="cuda") -> torch.Tensor:
+    """int32 [2 * max_distance + 1]: the bucket of each relative position (key - query) from
+    -max_distance to max_distance (see window_attention and include/vsa.h)."""
+    out = torch.empty(max(1, 2 * int(max_distance) + 1), dtype=torch.int32, device=device)
+    with torch.cuda.device(out.device):
+        _check(lib().vsa_relative_position_buckets(int(num_buckets), int(max_distance), _ptr(out), _stream(out.device)))
+    return out
 
 
 def cast_f32_to_bf16(x: torch.Tensor) -> torch.Tensor:
@@ -649,15 +945,14 @@ def spade_attention(q, k, v, grid, tiles, budget: Optional[float] = None, topk: 
                                   "tiled mode only (see tiled_supported)")
     choice = select_tiling(q, grid, tiles) if len(tiles) > 1 else None
     if tiled:
-        qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
         qmax, qmin = block_summaries_tiled(q, grid, tiles, choice, block)
         kmax, kmin = block_summaries_tiled(k, grid, tiles, choice, block)
         scores = block_scores(qmax, qmin, kmax, kmin)
         idx, cnt = _select_blocks(scores, kk, n_sink_blocks, diag_halfwidth, top_p, top_p_scale, D)
         if compensate:
-            o = centroid_compensated_attention_tiled(qb, kb, vb, grid, tiles, choice, idx, cnt, scale, out_dtype)
+            o = centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, out_dtype)
         else:
-            o = block_sparse_attention_tiled(qb, kb, vb, grid, tiles, choice, idx, cnt, scale, out_dtype)
+            o = block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, out_dtype)
         if return_intermediates:
             qp, kp, vp, op = (permute(x, grid, tiles, choice) for x in (q, k, v, o))
     else:

@@ -506,34 +506,33 @@ static vsa_status check_attention_common(const void *q, const void *k, const voi
     return VSA_OK;
 }
 
-vsa_status vsa_block_sparse_attention(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
-                                      int B, int n_heads, int S, int D, int block, const int32_t *idx,
-                                      const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
-                                      void *stream) {
-    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+// The launch of an attention call over block lists in tile-contiguous order
+// (the tensors are checked by the caller).
+static vsa_status lists_launch(const void *q, const void *k, const void *v, int B, int n_heads, int S, int D, int block,
+                               const int32_t *idx, const int32_t *cnt, int cap, int list_per_head, int group_size,
+                               float scale, AttnLaunch *out) {
     VSA_REQUIRE(block == 32 || block == 64 || block == 128, "block must be 32, 64 or 128, got %d", block);
     VSA_REQUIRE(S % block == 0, "block (%d) must divide S (%d)", block, S);
     VSA_REQUIRE(aligned4(idx) && aligned4(cnt), "idx and cnt must be non-NULL 4-byte aligned device pointers");
     VSA_REQUIRE(cap >= 1, "cap must be >= 1, got %d", cap);
     VSA_REQUIRE(group_size >= 0, "group_size must be >= 0, got %d", group_size);
     AttnLaunch L{};
-    L.q = q; L.k = k; L.v = v; L.o = o;
-    L.out_f32 = out_dtype == VSA_F32;
+    L.q = q; L.k = k; L.v = v;
     L.BH = B * n_heads; L.S = S; L.D = D;
     L.block = block;
     L.window = false;
     L.idx = idx; L.cnt = cnt; L.cap = cap; L.list_per_head = list_per_head ? 1 : 0;
     L.group = group_size; L.nb = S / block;
     L.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
-    return launch_attention(L, status_or_null(stream), as_stream(stream));
+    *out = L;
+    return VSA_OK;
 }
 
-vsa_status vsa_block_sparse_attention_tiled(const void *q, const void *k, const void *v, void *o,
-                                            vsa_dtype out_dtype, int B, int n_heads, int S, int D, vsa_dims3 grid,
-                                            const vsa_dims3 *tiles, int n_tiles, const int32_t *choice,
-                                            const int32_t *idx, const int32_t *cnt, int cap, int list_per_head,
-                                            int group_stride, float scale, void *stream) {
-    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+// The same over T-major tensors, each (b, head) in its own tiling.
+static vsa_status tiled_launch(const void *q, const void *k, const void *v, int B, int n_heads, int S, int D,
+                               vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles, const int32_t *choice,
+                               const int32_t *idx, const int32_t *cnt, int cap, int list_per_head, int group_stride,
+                               float scale, AttnLaunch *out) {
     VSA_REQUIRE(group_stride == 0 || (group_stride >= 2 && group_stride <= 128 && (group_stride & (group_stride - 1)) == 0),
                 "group_stride must be 0 or a power of two in [2, 128], got %d", group_stride);
     VSA_REQUIRE(aligned4(idx) && aligned4(cnt), "idx and cnt must be non-NULL 4-byte aligned device pointers");
@@ -563,8 +562,7 @@ vsa_status vsa_block_sparse_attention_tiled(const void *q, const void *k, const 
                         c, blk, ts.t[c] / (vol / blk), ts.h[c], ts.w[c], grid.t, grid.h, grid.w);
     }
     AttnLaunch L{};
-    L.q = q; L.k = k; L.v = v; L.o = o;
-    L.out_f32 = out_dtype == VSA_F32;
+    L.q = q; L.k = k; L.v = v;
     L.BH = B * n_heads; L.S = S; L.D = D;
     L.block = blk;
     L.window = false;
@@ -577,6 +575,51 @@ vsa_status vsa_block_sparse_attention_tiled(const void *q, const void *k, const 
     L.Tp = pg.t; L.Hp = pg.h; L.Wp = pg.w;
     L.tiles = ts;
     L.choice = choice;
+    *out = L;
+    return VSA_OK;
+}
+
+static vsa_status window_launch(const void *q, const void *k, const void *v, int B, int n_heads, int S, int D,
+                                int window, int sink, float scale, AttnLaunch *out) {
+    VSA_REQUIRE(window >= 1, "window must be >= 1, got %d", window);
+    VSA_REQUIRE(sink >= 0, "sink must be >= 0, got %d", sink);
+    VSA_REQUIRE(sink <= S, "sink (%d) cannot exceed sequence length (%d)", sink, S);
+    AttnLaunch L{};
+    L.q = q; L.k = k; L.v = v;
+    L.BH = B * n_heads; L.S = S; L.D = D;
+    L.block = 128;
+    L.window = true;
+    L.dense = window >= S ? 1 : 0;
+    L.half = window / 2;
+    L.sink = sink;
+    L.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
+    *out = L;
+    return VSA_OK;
+}
+
+vsa_status vsa_block_sparse_attention(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
+                                      int B, int n_heads, int S, int D, int block, const int32_t *idx,
+                                      const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
+                                      void *stream) {
+    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(lists_launch(q, k, v, B, n_heads, S, D, block, idx, cnt, cap, list_per_head, group_size, scale, &L));
+    L.o = o;
+    L.out_f32 = out_dtype == VSA_F32;
+    return launch_attention(L, status_or_null(stream), as_stream(stream));
+}
+
+vsa_status vsa_block_sparse_attention_tiled(const void *q, const void *k, const void *v, void *o,
+                                            vsa_dtype out_dtype, int B, int n_heads, int S, int D, vsa_dims3 grid,
+                                            const vsa_dims3 *tiles, int n_tiles, const int32_t *choice,
+                                            const int32_t *idx, const int32_t *cnt, int cap, int list_per_head,
+                                            int group_stride, float scale, void *stream) {
+    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(tiled_launch(q, k, v, B, n_heads, S, D, grid, tiles, n_tiles, choice, idx, cnt, cap, list_per_head,
+                         group_stride, scale, &L));
+    L.o = o;
+    L.out_f32 = out_dtype == VSA_F32;
     return launch_attention(L, status_or_null(stream), as_stream(stream));
 }
 
@@ -678,21 +721,265 @@ vsa_status vsa_window_attention(const void *q, const void *k, const void *v, voi
                                 int n_heads, int S, int D, int window, int sink, float scale, int chunk,
                                 void *stream) {
     VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
-    VSA_REQUIRE(window >= 1, "window must be >= 1, got %d", window);
-    VSA_REQUIRE(sink >= 0, "sink must be >= 0, got %d", sink);
-    VSA_REQUIRE(sink <= S, "sink (%d) cannot exceed sequence length (%d)", sink, S);
+    AttnLaunch L;
+    VSA_TRY(window_launch(q, k, v, B, n_heads, S, D, window, sink, scale, &L));
     VSA_REQUIRE(chunk >= 0, "chunk_size must be >= 1 (or 0 for the default), got %d", chunk);
-    AttnLaunch L{};
-    L.q = q; L.k = k; L.v = v; L.o = o;
+    L.o = o;
     L.out_f32 = out_dtype == VSA_F32;
-    L.BH = B * n_heads; L.S = S; L.D = D;
-    L.block = 128;
-    L.window = true;
-    L.dense = window >= S ? 1 : 0;
-    L.half = window / 2;
-    L.sink = sink;
-    L.scale = scale > 0.f ? scale : 1.0f / sqrtf(static_cast<float>(D));
     return launch_attention(L, status_or_null(stream), as_stream(stream));
+}
+
+// ---- training: forward passes that keep the log-sum-exp, and backward passes ----
+
+static vsa_status check_lse(const float *lse, const void *o, size_t o_bytes, const void *q, const void *k, const void *v,
+                            int BH, int S, int D) {
+    VSA_REQUIRE(aligned4(lse), "lse must be a non-NULL 4-byte aligned device pointer");
+    const size_t n = static_cast<size_t>(BH) * S * 4, in = static_cast<size_t>(BH) * S * D * 2;
+    VSA_REQUIRE(!overlaps(lse, n, o, o_bytes) && !overlaps(lse, n, q, in) && !overlaps(lse, n, k, in) &&
+                    !overlaps(lse, n, v, in),
+                "lse must not overlap q, k, v or o");
+    return VSA_OK;
+}
+
+static vsa_status check_workspace(const void *workspace, size_t bytes, size_t need) {
+    VSA_REQUIRE(workspace != nullptr && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+                "workspace must be a non-NULL 256-byte aligned device pointer");
+    VSA_REQUIRE(bytes >= need, "workspace holds %zu bytes, %zu needed", bytes, need);
+    return VSA_OK;
+}
+
+static vsa_status check_bias(const void *bias, vsa_dtype bias_dtype, int num_buckets, int max_distance) {
+    VSA_REQUIRE(aligned4(bias), "bias must be a non-NULL 4-byte aligned device pointer");
+    VSA_REQUIRE(bias_dtype == VSA_BF16 || bias_dtype == VSA_F32, "bias_dtype must be VSA_BF16 or VSA_F32");
+    VSA_REQUIRE(num_buckets >= 4 && num_buckets <= 256 && num_buckets % 2 == 0,
+                "num_buckets must be even and in [4, 256], got %d", num_buckets);
+    VSA_REQUIRE(max_distance > num_buckets / 4 && max_distance <= (1 << 24),
+                "max_distance must be in (num_buckets / 4, 2^24], got %d for %d buckets", max_distance, num_buckets);
+    return VSA_OK;
+}
+
+vsa_status vsa_block_sparse_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
+                                          float *lse, int B, int n_heads, int S, int D, int block, const int32_t *idx,
+                                          const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
+                                          void *stream) {
+    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(lists_launch(q, k, v, B, n_heads, S, D, block, idx, cnt, cap, list_per_head, group_size, scale, &L));
+    VSA_TRY(check_lse(lse, o, static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype), q, k, v, L.BH, S, D));
+    L.o = o;
+    L.out_f32 = out_dtype == VSA_F32;
+    L.lse = lse;
+    return launch_attention(L, status_or_null(stream), as_stream(stream));
+}
+
+vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, const void *v, void *o,
+                                                vsa_dtype out_dtype, float *lse, int B, int n_heads, int S, int D,
+                                                vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
+                                                const int32_t *choice, const int32_t *idx, const int32_t *cnt, int cap,
+                                                int list_per_head, int group_stride, float scale, void *stream) {
+    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(tiled_launch(q, k, v, B, n_heads, S, D, grid, tiles, n_tiles, choice, idx, cnt, cap, list_per_head,
+                         group_stride, scale, &L));
+    VSA_TRY(check_lse(lse, o, static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype), q, k, v, L.BH, S, D));
+    L.o = o;
+    L.out_f32 = out_dtype == VSA_F32;
+    L.lse = lse;
+    return launch_attention(L, status_or_null(stream), as_stream(stream));
+}
+
+size_t vsa_window_attention_lse_workspace_size(int n_heads, int S, int num_buckets, int max_distance) {
+    if (n_heads < 1 || S < 1 || num_buckets == 0) return 0;
+    if (num_buckets < 4 || num_buckets > 256 || num_buckets % 2 != 0) return 0;
+    if (max_distance <= num_buckets / 4 || max_distance > (1 << 24)) return 0;
+    return bias_workspace_bytes(n_heads, S, max_distance);
+}
+
+vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
+                                    float *lse, int B, int n_heads, int S, int D, int window, int sink, float scale,
+                                    const void *bias, vsa_dtype bias_dtype, int num_buckets, int max_distance,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(window_launch(q, k, v, B, n_heads, S, D, window, sink, scale, &L));
+    const size_t o_bytes = static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype);
+    if (lse) VSA_TRY(check_lse(lse, o, o_bytes, q, k, v, L.BH, S, D));
+    L.o = o;
+    L.out_f32 = out_dtype == VSA_F32;
+    L.lse = lse;
+    if (bias) {
+        VSA_TRY(check_bias(bias, bias_dtype, num_buckets, max_distance));
+        const size_t need = vsa_window_attention_lse_workspace_size(n_heads, S, num_buckets, max_distance);
+        const size_t in = static_cast<size_t>(L.BH) * S * D * 2;
+        VSA_TRY(check_workspace(workspace, workspace_bytes, need));
+        VSA_REQUIRE(!overlaps(workspace, need, o, o_bytes) && !overlaps(workspace, need, q, in) &&
+                        !overlaps(workspace, need, k, in) && !overlaps(workspace, need, v, in) &&
+                        !(lse && overlaps(workspace, need, lse, static_cast<size_t>(L.BH) * S * 4)) &&
+                        !overlaps(workspace, need, bias,
+                                  static_cast<size_t>(num_buckets) * n_heads * esize_of(bias_dtype)),
+                    "workspace must not overlap q, k, v, o, lse or bias");
+        L.n_heads = n_heads;
+        L.bias_R = bias_reach(S, max_distance);
+        VSA_TRY(check_cuda(launch_bias_expand(bias, bias_dtype == VSA_F32, n_heads, S, num_buckets, max_distance,
+                                              workspace, &L.bias_E, &L.bias_bm, as_stream(stream)),
+                           "relative bias launch"));
+    }
+    return launch_attention(L, status_or_null(stream), as_stream(stream));
+}
+
+vsa_status vsa_relative_position_buckets(int num_buckets, int max_distance, int32_t *out, void *stream) {
+    VSA_TRY(check_bias(out, VSA_F32, num_buckets, max_distance));
+    return check_cuda(launch_bias_buckets(num_buckets, max_distance, out, as_stream(stream)),
+                      "relative_position_buckets launch");
+}
+
+size_t vsa_transpose_block_lists_workspace_size(int lists, int nb) {
+    if (lists < 1 || nb < 1) return 0;
+    return (transpose_lists_workspace_bytes(lists, nb) + 255) & ~static_cast<size_t>(255);
+}
+
+vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap,
+                                     int32_t *offsets, int32_t *rows, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    VSA_REQUIRE(lists >= 1 && lists <= 65535, "lists must be in [1, 65535], got %d", lists);
+    VSA_REQUIRE(nb >= 1 && nb <= (1 << 26), "nb must be in [1, 2^26], got %d", nb);
+    VSA_REQUIRE(cap >= 1, "cap must be >= 1, got %d", cap);
+    VSA_REQUIRE(static_cast<long long>(nb) * cap <= 0x7fffffffLL, "nb * cap must be < 2^31");
+    VSA_REQUIRE(aligned4(idx) && aligned4(cnt), "idx and cnt must be non-NULL 4-byte aligned device pointers");
+    VSA_REQUIRE(aligned4(offsets) && aligned4(rows), "offsets and rows must be non-NULL 4-byte aligned device pointers");
+    const size_t need = vsa_transpose_block_lists_workspace_size(lists, nb);
+    VSA_TRY(check_workspace(workspace, workspace_bytes, need));
+    const size_t n_idx = static_cast<size_t>(lists) * nb * cap * 4, n_cnt = static_cast<size_t>(lists) * nb * 4,
+                 n_off = static_cast<size_t>(lists) * (nb + 1) * 4;
+    VSA_REQUIRE(!overlaps(offsets, n_off, idx, n_idx) && !overlaps(offsets, n_off, cnt, n_cnt) &&
+                    !overlaps(rows, n_idx, idx, n_idx) && !overlaps(rows, n_idx, cnt, n_cnt) &&
+                    !overlaps(rows, n_idx, offsets, n_off) && !overlaps(workspace, need, idx, n_idx) &&
+                    !overlaps(workspace, need, cnt, n_cnt) && !overlaps(workspace, need, offsets, n_off) &&
+                    !overlaps(workspace, need, rows, n_idx),
+                "offsets, rows and workspace must not overlap one another, idx or cnt");
+    return check_cuda(launch_transpose_lists(idx, cnt, lists, nb, cap, offsets, rows, true, workspace,
+                                             status_or_null(stream), as_stream(stream)),
+                      "transpose_block_lists launch");
+}
+
+// Checks of a backward pass beyond the launch's own, then the launch.
+static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+                           void *dv, vsa_dtype grad_dtype, int B, int n_heads, const AttnLaunch &L, const void *bias,
+                           vsa_dtype bias_dtype, int num_buckets, int max_distance, void *dbias, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    const int BH = B * n_heads;
+    VSA_REQUIRE(o_dtype == VSA_BF16 || o_dtype == VSA_F32, "o_dtype must be VSA_BF16 or VSA_F32");
+    VSA_REQUIRE(aligned16(g) && aligned16(o), "dout and o must be non-NULL 16-byte aligned device pointers");
+    VSA_REQUIRE(aligned4(lse), "lse must be a non-NULL 4-byte aligned device pointer");
+    if (!L.window)
+        VSA_REQUIRE(static_cast<long long>(L.nb) * L.cap <= 0x7fffffffLL, "nb * cap must be < 2^31");
+    VSA_REQUIRE(static_cast<long long>(BH) * ((L.tiled ? L.nb : (L.S + L.block - 1) / L.block)) <= 0x7fffffffLL,
+                "too many blocks for one launch");
+    if (bias) VSA_TRY(check_bias(bias, bias_dtype, num_buckets, max_distance));
+    VSA_REQUIRE(bias != nullptr || dbias == nullptr, "dbias needs a bias");
+    VSA_REQUIRE(dbias == nullptr || aligned4(dbias), "dbias must be NULL or 4-byte aligned");
+    const int positions = L.tiled ? L.Tp * L.Hp * L.Wp : L.S;
+    const size_t need = backward_workspace_bytes(BH, n_heads, positions, L.S, L.window ? 0 : L.list_per_head ? BH : 1,
+                                                 L.nb, L.cap, bias ? num_buckets : 0, max_distance);
+    VSA_TRY(check_workspace(workspace, workspace_bytes, need));
+    // every output apart from every other buffer
+    const size_t n = static_cast<size_t>(BH) * L.S * L.D;
+    const size_t table = bias ? static_cast<size_t>(num_buckets) * n_heads * esize_of(bias_dtype) : 0;
+    const size_t lists = L.window ? 0 : static_cast<size_t>(L.list_per_head ? BH : 1) * L.nb;
+    const struct { const void *p; size_t n; } buf[] = {
+        {dq, n * esize_of(grad_dtype)}, {dk, n * esize_of(grad_dtype)}, {dv, n * esize_of(grad_dtype)},
+        {workspace, need}, {dbias, dbias ? table : 0},
+        {L.q, n * 2}, {L.k, n * 2}, {L.v, n * 2}, {g, n * 2}, {o, n * esize_of(o_dtype)},
+        {lse, static_cast<size_t>(BH) * L.S * 4}, {bias, table}, {L.idx, lists * L.cap * 4}, {L.cnt, lists * 4}};
+    for (int x = 0; x < 5; ++x)
+        for (int y = x + 1; y < 14; ++y)
+            VSA_REQUIRE(buf[x].n == 0 || buf[y].n == 0 || !overlaps(buf[x].p, buf[x].n, buf[y].p, buf[y].n),
+                        "dq, dk, dv, dbias and workspace must not overlap one another or an input");
+    BackwardLaunch W{};
+    W.a = L;
+    W.g = g;
+    W.o = o;
+    W.o_f32 = o_dtype == VSA_F32;
+    W.lse = lse;
+    W.dq = dq;
+    W.dk = dk;
+    W.dv = dv;
+    W.grad_f32 = grad_dtype == VSA_F32;
+    W.H = n_heads;
+    W.bias = bias;
+    W.bias_f32 = bias_dtype == VSA_F32;
+    W.buckets = num_buckets;
+    W.far = max_distance;
+    W.dbias = dbias;
+    return launch_backward(W, workspace, status_or_null(stream), as_stream(stream));
+}
+
+// check_attention_common for a backward pass: the three gradients in place of o
+static vsa_status check_gradients(const void *q, const void *k, const void *v, void *dq, void *dk, void *dv,
+                                  vsa_dtype grad_dtype, int B, int n_heads, int S, int D, float scale) {
+    VSA_TRY(check_bhsd(B, n_heads, S, D));
+    VSA_TRY(check_d(D));
+    VSA_REQUIRE(grad_dtype == VSA_BF16 || grad_dtype == VSA_F32, "grad_dtype must be VSA_BF16 or VSA_F32");
+    VSA_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v), "q, k and v must be non-NULL 16-byte aligned device pointers");
+    VSA_REQUIRE(aligned16(dq) && aligned16(dk) && aligned16(dv),
+                "dq, dk and dv must be non-NULL 16-byte aligned device pointers");
+    VSA_REQUIRE(scale == scale && scale < 3.0e38f, "scale must be finite");
+    return VSA_OK;
+}
+
+size_t vsa_block_sparse_attention_backward_workspace_size(int B, int n_heads, int positions, int block, int cap,
+                                                          int list_per_head) {
+    if (B < 1 || n_heads < 1 || static_cast<long long>(B) * n_heads > 65535 || positions < 1 || cap < 1) return 0;
+    if ((block != 32 && block != 64 && block != 128) || positions % block != 0) return 0;
+    const int BH = B * n_heads;
+    return backward_workspace_bytes(BH, n_heads, positions, positions, list_per_head ? BH : 1, positions / block, cap, 0, 0);
+}
+
+vsa_status vsa_block_sparse_attention_backward(const void *dout, const void *q, const void *k, const void *v,
+                                               const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+                                               void *dv, vsa_dtype grad_dtype, int B, int n_heads, int S, int D,
+                                               int block, const int32_t *idx, const int32_t *cnt, int cap,
+                                               int list_per_head, int group_size, float scale, void *workspace,
+                                               size_t workspace_bytes, void *stream) {
+    VSA_TRY(check_gradients(q, k, v, dq, dk, dv, grad_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(lists_launch(q, k, v, B, n_heads, S, D, block, idx, cnt, cap, list_per_head, group_size, scale, &L));
+    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
+                    workspace, workspace_bytes, stream);
+}
+
+vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const void *q, const void *k, const void *v,
+                                                     const void *o, vsa_dtype o_dtype, const float *lse, void *dq,
+                                                     void *dk, void *dv, vsa_dtype grad_dtype, int B, int n_heads,
+                                                     int S, int D, vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
+                                                     const int32_t *choice, const int32_t *idx, const int32_t *cnt,
+                                                     int cap, int list_per_head, int group_stride, float scale,
+                                                     void *workspace, size_t workspace_bytes, void *stream) {
+    VSA_TRY(check_gradients(q, k, v, dq, dk, dv, grad_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(tiled_launch(q, k, v, B, n_heads, S, D, grid, tiles, n_tiles, choice, idx, cnt, cap, list_per_head,
+                         group_stride, scale, &L));
+    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
+                    workspace, workspace_bytes, stream);
+}
+
+size_t vsa_window_attention_backward_workspace_size(int B, int n_heads, int S, int num_buckets, int max_distance) {
+    if (B < 1 || n_heads < 1 || static_cast<long long>(B) * n_heads > 65535 || S < 1) return 0;
+    if (num_buckets != 0 && vsa_window_attention_lse_workspace_size(n_heads, S, num_buckets, max_distance) == 0) return 0;
+    return backward_workspace_bytes(B * n_heads, n_heads, S, S, 0, 0, 0, num_buckets, max_distance);
+}
+
+vsa_status vsa_window_attention_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
+                                         vsa_dtype o_dtype, const float *lse, void *dq, void *dk, void *dv,
+                                         vsa_dtype grad_dtype, int B, int n_heads, int S, int D, int window, int sink,
+                                         float scale, const void *bias, vsa_dtype bias_dtype, int num_buckets,
+                                         int max_distance, void *dbias, void *workspace, size_t workspace_bytes,
+                                         void *stream) {
+    VSA_TRY(check_gradients(q, k, v, dq, dk, dv, grad_dtype, B, n_heads, S, D, scale));
+    AttnLaunch L;
+    VSA_TRY(window_launch(q, k, v, B, n_heads, S, D, window, sink, scale, &L));
+    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, bias, bias_dtype, num_buckets,
+                    max_distance, dbias, workspace, workspace_bytes, stream);
 }
 
 vsa_status vsa_cast_f32_to_bf16(const float *x, void *y, int64_t n, void *stream) {

@@ -46,6 +46,7 @@ struct AttnArgs {
     float scale_log2;
     void *out;
     int out_f32;
+    float *lse;  // optional per-row log-sum-exp, see AttnLaunch
     int *status;
     // tiled mode
     int H, W;  // the padded grid's frame
@@ -509,7 +510,10 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
                 }
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);  // empty key set
+            if (a.lse && row_valid)
+                a.lse[orow] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : l_sum == 0.f ? -INFINITY : l_sum;
         } else if (row_valid && !list_valid) {
+            if (a.lse) a.lse[orow] = -INFINITY;
             // invalid list: the row is written as zeros
             if (a.out_f32) {
                 float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
@@ -569,6 +573,7 @@ vsa_status run(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.out = L.o;
     a.out_f32 = L.out_f32;
+    a.lse = L.lse;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;

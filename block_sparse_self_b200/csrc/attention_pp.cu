@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "relative_bias.cuh"
 
 namespace vsa {
 
@@ -54,6 +55,10 @@ struct PPArgs {
     void *out;
     int out_f32;
     float2 *stats;  // optional per-row (m, l), see AttnLaunch
+    float *lse;     // optional per-row log-sum-exp, see AttnLaunch
+    const float *bias_E;  // window mode with a relative position bias: log2e bias by offset,
+    const uint8_t *bias_bm;  // and bucket by offset (see relative_bias.cu)
+    int bias_R, n_heads;
     int *status;
     // tiled mode: T-major tensors, per-head tiling (all of volume 128 * m)
     int H, W;         // the padded grid's frame (equal to the real one when nothing is padded)
@@ -155,9 +160,18 @@ __device__ __forceinline__ int kblock_of(const TileSched &t, int j) {
     else return __ldg(t.list + j);
 }
 
+// The row's log-sum-exp from its softmax state in the log2 domain.
+__device__ __forceinline__ float row_lse(float m, float l) {
+    return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l);
+}
+
 // PAD (tiled mode only): the grid is zero-padded, so padding rows and keys need
 // handling; a separate instantiation keeps that code out of the common case.
-template <int D, bool WINDOW, bool TILED, bool PAD>
+// BIAS (window mode only): a relative position bias is added to the logits,
+// one value per tile where its offsets share a bucket, else by shuffles (see
+// relative_bias.cuh).  S then becomes scale*log2e*S + bias on its way
+// out of tensor memory and the softmax below runs with a scale of 1.
+template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     using C = PPCfg<D>;
@@ -412,7 +426,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         }
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t s_col = t * 128, o_col = C::O_COL + t * D;
-        const float sl2 = a.scale_log2;
+        const float sl2 = BIAS ? 1.f : a.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -445,6 +459,34 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                     }
                 }
             }
+            auto apply_bias = [&]() {
+                if constexpr (BIAS) {
+                    const float *E = a.bias_E + static_cast<size_t>(bh % a.n_heads) * (2 * a.bias_R + 1) + a.bias_R;
+                    const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
+                    int bucket;
+                    if (bias_uniform(a.bias_bm + a.bias_R, a.bias_R, d, bucket)) {
+                        const float b = __ldg(E + min(max(d, -a.bias_R), a.bias_R));
+                        const uint64_t sx = f32x2(a.scale_log2, a.scale_log2), bx = f32x2(b, b);
+                        #pragma unroll
+                        for (int c = 0; c < BN; c += 2) {
+                            float y0, y1;
+                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sx, bx), y0, y1);
+                            x[c] = __float_as_uint(y0);
+                            x[c + 1] = __float_as_uint(y1);
+                        }
+                    } else {
+                        #pragma unroll
+                        for (int u = 0; u < BN / 32; ++u) {
+                            const BiasPiece piece = bias_piece(E, a.bias_R, 1, d + 32 * u - wq * 32, lane);
+                            #pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                x[32 * u + i] = __float_as_uint(fmaf(__uint_as_float(x[32 * u + i]), a.scale_log2,
+                                                                     bias_at(piece, i, lane)));
+                        }
+                    }
+                }
+            };
+            apply_bias();
             auto apply_mask = [&]() {
                 if constexpr (WINDOW) {
                     const int ks = kblock_of<WINDOW>(sc, j) * BN;
@@ -533,6 +575,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 for (int c = 0; c < BN / 32; ++c)
                     tmem_ld32(t_lane + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
                 tmem_ld_wait();
+                apply_bias();
                 apply_mask();
                 const float m_new = need ? fmaxf(m_ref, raw_max() * sl2) : m_ref;
                 if (j > 0) {
@@ -606,8 +649,10 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);
             if (a.stats && row_valid) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(m_ref, l_sum);
+            if (a.lse && row_valid) a.lse[orow] = row_lse(m_ref, l_sum);
         } else if (row_valid && bad[t]) {
             if (a.stats) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(-INFINITY, 0.f);
+            if (a.lse) a.lse[orow] = -INFINITY;
             if (a.out_f32) {
                 float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
                 for (int e = 0; e < D / 4; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -626,7 +671,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     }
 }
 
-template <int D, bool WINDOW, bool TILED, bool PAD = false>
+template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false>
 vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     using C = PPCfg<D>;
     MapSet maps = {};  // copied into the launch parameters
@@ -645,7 +690,7 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
              make_tile_map(&maps.v[0], L.v, D, L.S, L.BH, 128);
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
-    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD>;
+    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention, two tiles)");
     PPArgs a;
@@ -669,6 +714,11 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.out = L.o;
     a.out_f32 = L.out_f32;
     a.stats = L.stats;
+    a.lse = L.lse;
+    a.bias_E = L.bias_E;
+    a.bias_bm = L.bias_bm;
+    a.bias_R = L.bias_R;
+    a.n_heads = L.n_heads;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;
@@ -940,6 +990,7 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             if (sc.n == 0) {
                 if (row_valid && T.bad) {
                     if (a.stats) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(-INFINITY, 0.f);
+                    if (a.lse) a.lse[orow] = -INFINITY;
                     if (a.out_f32) {
                         float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
                         for (int e = 0; e < D / 4; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1061,6 +1112,7 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);
             if (a.stats && row_valid) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(m_ref, l_sum);
+            if (a.lse && row_valid) a.lse[orow] = row_lse(m_ref, l_sum);
             ++w;
         }
         if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
@@ -1121,6 +1173,11 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.out = L.o;
     a.out_f32 = L.out_f32;
     a.stats = L.stats;
+    a.lse = L.lse;
+    a.bias_E = L.bias_E;
+    a.bias_bm = L.bias_bm;
+    a.bias_R = L.bias_R;
+    a.n_heads = L.n_heads;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;
@@ -1172,6 +1229,9 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
 }  // namespace
 
 vsa_status launch_attention_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
+    if (L.window && L.bias_E)
+        return L.D == 128 ? run_pp<128, true, false, false, true>(L, status, st)
+                          : run_pp<64, true, false, false, true>(L, status, st);
     if (L.window) return L.D == 128 ? run_pp<128, true, false>(L, status, st) : run_pp<64, true, false>(L, status, st);
     if (L.cap == 1) {  // lists of one key block
         if (L.tiled) {

@@ -1,0 +1,262 @@
+// backward.cu -- the steps around the backward pass's two tensor-core passes:
+// per-row statistics, workspace, tensor maps and launches.
+//
+// Row statistics: delta_i = g_i.o_i, one pass over g and o (bandwidth bound:
+// 2 x 2 S D bytes per head in bf16), written in position order beside -lse so
+// that both passes read 128 consecutive values per tile whatever the tiling.
+// Positions that hold no token and rows whose forward pass saw no key get
+// -lse = -inf, i.e. P = 0 everywhere: they reach no gradient.
+#include "backward.cuh"
+
+namespace vsa {
+
+namespace {
+
+struct StatArgs {
+    const void *o, *g;
+    const float *lse;
+    int P, Pw, S_out;
+    TileDivs divs[kMaxTiles];
+    RealGrid real;
+    int tiled, n_tiles;
+    const int32_t *choice;
+    float *nlse, *ndelta, *none;
+    uint32_t *valid;  // nullptr when every position holds a token
+};
+
+// A warp takes 32 consecutive positions of one head, 32 / LPR rows at a time
+// (LPR lanes of 16 bytes of g per row).
+template <int D, bool O_F32>
+__global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ StatArgs a) {
+    constexpr int LPR = D / 8, ROWS = 32 / LPR;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
+    if (blockIdx.x == 0 && bh == 0) a.none[threadIdx.x] = threadIdx.x < 128 ? -INFINITY : 0.f;
+    const int p0 = (blockIdx.x * 8 + warp) * 32;
+    if (p0 >= a.Pw) return;
+    const int p = p0 + lane;
+    int tok = p < a.P ? p : -1;
+    if (a.tiled && tok >= 0) {
+        int tc = a.choice ? __ldg(a.choice + bh) : 0;
+        if (tc < 0 || tc >= a.n_tiles) tc = 0;  // the head is not computed
+        uint32_t t, h, w;
+        tile_coords_fast(p, a.divs[tc], t, h, w);
+        tok = real_token(t, h, w, a.real);
+    }
+    const uint32_t bits = __ballot_sync(0xffffffffu, tok >= 0);
+    if (a.valid && lane == 0) a.valid[static_cast<size_t>(bh) * (a.Pw / 32) + p0 / 32] = bits;
+    const int sub = lane / LPR, at = lane % LPR;
+    float delta = 0.f;
+    #pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += ROWS) {
+        const int rt = __shfl_sync(0xffffffffu, tok, r0 + sub);
+        float s = 0.f;
+        if (rt >= 0) {
+            const size_t e = (static_cast<size_t>(bh) * a.S_out + rt) * D + at * 8;
+            const uint4 g4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.g) + e));
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            float o[8];
+            if constexpr (O_F32) {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.o) + e);
+                const float4 x = __ldg(src), y = __ldg(src + 1);
+                o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+                o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
+            } else {
+                const uint4 o4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + e));
+                const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    o[2 * c] = __uint_as_float(ow[c] << 16);
+                    o[2 * c + 1] = __uint_as_float(ow[c] & 0xffff0000u);
+                }
+            }
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                s = fmaf(__uint_as_float(gw[c] << 16), o[2 * c], s);
+                s = fmaf(__uint_as_float(gw[c] & 0xffff0000u), o[2 * c + 1], s);
+            }
+        }
+        #pragma unroll
+        for (int x = LPR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        // lane r0 + u keeps row r0 + u's sum, held by the lanes of group u
+        #pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+            const float v = __shfl_sync(0xffffffffu, s, u * LPR);
+            if (lane == r0 + u) delta = v;
+        }
+    }
+    float nl = -INFINITY;
+    if (tok >= 0) {
+        const float l = __ldg(a.lse + static_cast<size_t>(bh) * a.S_out + tok);
+        // -inf: no key was seen, no gradient.  +inf and NaN have no finite
+        // softmax to differentiate; NaN lets the gradients show it.
+        nl = l == -INFINITY ? -INFINITY : l == INFINITY ? NAN : -l * 1.4426950408889634f;
+    }
+    if (nl == -INFINITY) delta = 0.f;
+    const size_t out = static_cast<size_t>(bh) * a.Pw + p;
+    a.nlse[out] = nl;
+    a.ndelta[out] = -delta;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Layout {
+    size_t nlse, ndelta, none, valid, t_off, t_rows, bits, part, bias, total;
+};
+
+Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far) {
+    const size_t Pw = (static_cast<size_t>(positions) + 127) / 128 * 128;
+    Layout L{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    L.nlse = take(BH * Pw * 4);
+    L.ndelta = take(BH * Pw * 4);
+    L.none = take(256 * 4);
+    L.valid = take(BH * (Pw / 32) * 4);
+    if (lists > 0) {
+        L.t_off = take(static_cast<size_t>(lists) * (nb + 1) * 4);
+        L.t_rows = take(static_cast<size_t>(lists) * nb * cap * 4);
+        L.bits = take(transpose_lists_workspace_bytes(lists, nb));
+    }
+    if (buckets > 0) {
+        L.part = take(BH * (Pw / 128) * 8 * static_cast<size_t>(buckets) * 4);
+        L.bias = take(bias_workspace_bytes(H, S, far));
+    }
+    L.total = at;
+    return L;
+}
+
+}  // namespace
+
+size_t backward_workspace_bytes(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far) {
+    return layout(BH, H, positions, S, lists, nb, cap, buckets, far).total;
+}
+
+vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status, cudaStream_t st) {
+    const AttnLaunch &L = B.a;
+    const int positions = L.tiled ? L.Tp * L.Hp * L.Wp : L.S;
+    const int lists = L.window ? 0 : L.list_per_head ? L.BH : 1;
+    const int buckets = B.bias ? B.buckets : 0;
+    const Layout lay = layout(L.BH, B.H, positions, L.S, lists, L.nb, L.cap, buckets, B.far);
+    char *ws = static_cast<char *>(workspace);
+    auto f32_at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+
+    BwdArgs a{};
+    a.P = positions;
+    a.Pw = (positions + 127) / 128 * 128;
+    a.S_out = L.S;
+    a.BH = L.BH;
+    a.H = B.H;
+    a.nt = (positions + L.block - 1) / L.block;
+    a.idx = L.idx;
+    a.cnt = L.cnt;
+    a.cap = L.cap;
+    a.list_per_head = L.list_per_head;
+    a.nb = L.nb;
+    a.group = L.group;
+    a.gstride = L.gstride;
+    a.half = L.half;
+    a.sink = L.sink;
+    a.dense = L.dense;
+    a.scale = L.scale;
+    a.scale_log2 = L.scale * 1.4426950408889634f;
+    a.nlse = f32_at(lay.nlse);
+    a.ndelta = f32_at(lay.ndelta);
+    a.none = f32_at(lay.none);
+    a.out_f32 = B.grad_f32;
+    a.status = status;
+    a.real = RealGrid{L.T, L.Hg, L.Wg};
+    a.tiles = L.tiles;
+    a.choice = L.choice;
+    a.H2 = L.Hp;
+    a.W2 = L.Wp;
+    const bool padded = L.tiled && positions != L.S;
+    if (padded) a.valid = reinterpret_cast<const uint32_t *>(ws + lay.valid);
+
+    StatArgs s{};
+    s.o = B.o;
+    s.g = B.g;
+    s.lse = B.lse;
+    s.P = a.P;
+    s.Pw = a.Pw;
+    s.S_out = L.S;
+    s.real = a.real;
+    s.tiled = L.tiled;
+    s.n_tiles = L.tiles.n;
+    s.choice = L.choice;
+    s.nlse = f32_at(lay.nlse);
+    s.ndelta = f32_at(lay.ndelta);
+    s.none = f32_at(lay.none);
+    s.valid = padded ? reinterpret_cast<uint32_t *>(ws + lay.valid) : nullptr;
+
+    BwdMaps maps = {};
+    bool ok = true;
+    if (L.tiled) {
+        for (int c = 0; c < L.tiles.n; ++c) {
+            const int tt = L.tiles.t[c], th = L.tiles.h[c], tw = L.tiles.w[c], m = tt * th * tw / L.block;
+            s.divs[c] = make_tile_divs(L.Hp, L.Wp, tt, th, tw);
+            auto &g = a.geom[c];
+            g.m = make_fastdiv(m);
+            g.nthw = make_fastdiv((L.Hp / th) * (L.Wp / tw));
+            g.ntw = make_fastdiv(L.Wp / tw);
+            g.bt = tt / m;
+            // the real tensors: boxes reaching past them read zeros
+            const struct { CUtensorMap *m; const void *x; } four[4] = {
+                {&maps.q[c], L.q}, {&maps.k[c], L.k}, {&maps.v[c], L.v}, {&maps.g[c], B.g}};
+            for (auto &f : four) ok = ok && make_box_map(f.m, f.x, L.D, L.T, L.Hg, L.Wg, L.BH, g.bt, th, tw);
+        }
+    } else {
+        ok = make_tile_map(&maps.q[0], L.q, L.D, L.S, L.BH, L.block) &&
+             make_tile_map(&maps.k[0], L.k, L.D, L.S, L.BH, L.block) &&
+             make_tile_map(&maps.v[0], L.v, L.D, L.S, L.BH, L.block) &&
+             make_tile_map(&maps.g[0], B.g, L.D, L.S, L.BH, L.block);
+    }
+    if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
+
+    if (buckets > 0) {
+        const vsa_status r = check_cuda(launch_bias_expand(B.bias, B.bias_f32, B.H, L.S, buckets, B.far, ws + lay.bias,
+                                                           &a.E, &a.bm, st),
+                                        "relative bias launch");
+        if (r != VSA_OK) return r;
+        a.R = bias_reach(L.S, B.far);
+        a.buckets = buckets;
+        a.dbias_part = B.dbias ? f32_at(lay.part) : nullptr;
+    }
+    const dim3 grid((a.Pw / 32 + 7) / 8, L.BH);
+    if (L.D == 128) {
+        if (B.o_f32) row_stats_kernel<128, true><<<grid, 256, 0, st>>>(s);
+        else row_stats_kernel<128, false><<<grid, 256, 0, st>>>(s);
+    } else {
+        if (B.o_f32) row_stats_kernel<64, true><<<grid, 256, 0, st>>>(s);
+        else row_stats_kernel<64, false><<<grid, 256, 0, st>>>(s);
+    }
+    vsa_status r = check_cuda(cudaGetLastError(), "attention backward launch (row statistics)");
+    if (r != VSA_OK) return r;
+    if (lists > 0) {
+        int32_t *off = reinterpret_cast<int32_t *>(ws + lay.t_off), *rows = reinterpret_cast<int32_t *>(ws + lay.t_rows);
+        r = check_cuda(launch_transpose_lists(L.idx, L.cnt, lists, L.nb, L.cap, off, rows, false, ws + lay.bits, status, st),
+                       "attention backward launch (transposed lists)");
+        if (r != VSA_OK) return r;
+        a.t_off = off;
+        a.t_rows = rows;
+    }
+    // the key blocks that the sinks are in are listed by every query block
+    a.lead = L.window ? (L.dense ? 0 : (L.sink + 127) / 128) : 1;
+    if (a.lead > a.nt) a.lead = a.nt;
+    a.d0 = B.dq;
+    r = launch_bwd_dq(maps, a, L.D, L.block, L.window, L.tiled, buckets > 0, st);
+    if (r != VSA_OK) return r;
+    a.d0 = B.dk;
+    a.d1 = B.dv;
+    r = launch_bwd_dkv(maps, a, L.D, L.block, L.window, L.tiled, buckets > 0, st);
+    if (r != VSA_OK) return r;
+    if (a.dbias_part)
+        r = check_cuda(launch_dbias(a.dbias_part, L.BH / B.H, B.H, a.nt * 8, buckets, B.dbias, B.bias_f32, st),
+                       "relative bias gradient launch");
+    return r;
+}
+
+}  // namespace vsa

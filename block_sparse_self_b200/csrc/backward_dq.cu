@@ -1,0 +1,496 @@
+// backward_dq.cu -- dQ of block-sparse and sliding-window attention, and the
+// gradient of a relative position bias, on tcgen05 tensor cores: one CTA per
+// (query block, batch x head), walking the key blocks of its list (see
+// backward.cuh for the mathematics).
+//
+// Queries along the rows: per tile of 128 keys
+//   S = Q K^T, dP = g V^T                  (shared-memory operands)
+//   P = 2^(scale_log2 S - lse), dX = P (dP - delta)    (registers)
+//   dQ += dX K                             (dX is a tensor-memory operand)
+// Q and g stay in shared memory, K and V are streamed.  Tensor memory at
+// D = 128: two S buffers, dP and dQ.  dX (bf16) is written over the S it came
+// from, so the next tile's S is computed while this one is worked on, and dP
+// is refilled as soon as it has been read.
+//
+// dbias: dX summed by the bucket of j - i, in fp32 from unrounded values.  A
+// tile whose offsets share one bucket (most do: buckets widen with distance)
+// adds its row sums to one register, written out when the bucket changes; in
+// the others each warp sums its diagonals by shuffles (element (r, i) goes to
+// the lane of its diagonal) and then runs of equal buckets.  Every warp has
+// its own row of partial sums, added in a fixed order by a later kernel.
+#include "backward.cuh"
+
+namespace vsa {
+
+namespace {
+
+template <int D>
+struct DqCfg {
+    static constexpr int TILE = 128 * D * 2;
+    static constexpr int NK = D == 128 ? 3 : 4;  // ring of K tiles
+    static constexpr int NV = D == 128 ? 2 : 4;  // ring of V tiles
+    static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 2 + 4;
+    static constexpr int SMEM = 1024 + (2 + NK + NV) * TILE + N_BARS * 8 + 16;
+    static_assert(SMEM <= 232448, "shared memory");
+    static constexpr int DP_COL = 256, DQ_COL = 384;  // S buffers at 0 and 128
+};
+
+template <bool WINDOW>
+struct KeyWalk {
+    int n, r0_len, r1_start;  // window: key tiles [0, r0_len), then from r1_start on
+    const int32_t *list;
+    int count;
+    __device__ __forceinline__ int at(int x) const {
+        if constexpr (WINDOW) return x < r0_len ? x : r1_start + (x - r0_len);
+        else return __ldg(list + x);
+    }
+};
+
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
+    using C = DqCfg<D>;
+    constexpr int SLAB = 128 * 128, NSUB = 128 / BS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = base, *sG = sQ + C::TILE;
+    uint8_t *sK = sG + C::TILE;
+    uint8_t *sV = sK + C::NK * C::TILE;
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(sV + C::NV * C::TILE);
+    uint64_t *k_full = q_full + 1, *k_empty = k_full + C::NK;
+    uint64_t *v_full = k_empty + C::NK, *v_empty = v_full + C::NV;
+    uint64_t *s_full = v_empty + C::NV;  // [2]
+    uint64_t *dp_full = s_full + 2, *ds_full = dp_full + 1, *dq_done = ds_full + 1, *mma_done = dq_done + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *list_ok = reinterpret_cast<int *>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int qb = blockIdx.x, bh = blockIdx.y;
+    KeyWalk<WINDOW> w{};
+    if constexpr (WINDOW) {
+        const int q0 = qb * 128;
+        if (a.dense) {
+            w.r0_len = w.n = a.nt;
+        } else {
+            const int lo = max(0, q0 - a.half), hi = min(a.P, min(q0 + 128, a.P) + a.half);
+            const int lb0 = lo / 128, lb1 = (hi + 127) / 128, sb = (a.sink + 127) / 128;
+            if (sb == 0) {
+                w.r1_start = lb0;
+                w.n = lb1 - lb0;
+            } else if (lb0 <= sb) {
+                w.n = w.r0_len = max(lb1, sb);
+            } else {
+                w.r0_len = sb;
+                w.r1_start = lb0;
+                w.n = sb + (lb1 - lb0);
+            }
+        }
+        w.count = w.n;
+    } else {
+        const size_t lrow = (a.list_per_head ? static_cast<size_t>(bh) * a.nb : 0) + qb;
+        w.list = a.idx + lrow * a.cap;
+        w.count = __ldg(a.cnt + lrow);
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < C::NK; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < C::NV; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 8);
+        mbar_init(dq_done, 1);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if constexpr (!WINDOW) {
+        if (warp == 0) {
+            bool ok = w.count >= 1 && w.count <= a.cap;
+            if (ok) {
+                for (int j = lane; j < w.count; j += 32) {
+                    const int v = __ldg(w.list + j);
+                    ok = ok && v >= 0 && v < a.nb && (j == 0 || __ldg(w.list + j - 1) < v);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (lane == 0) *list_ok = ok ? 1 : 0;
+        }
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool head_ok = true;
+    int tc = 0;
+    if constexpr (!WINDOW) {
+        if (!*list_ok) {  // the rows get zeros
+            w.count = 0;
+            if (threadIdx.x == 0) report(a.status, DEV_RUNTIME);
+        }
+    }
+    if constexpr (TILED) {
+        if (a.choice) tc = __ldg(a.choice + bh);
+        if (tc < 0 || tc >= a.tiles.n) {  // the head is left unwritten
+            if (threadIdx.x == 0) report(a.status, DEV_RUNTIME);
+            head_ok = false;
+            w.count = 0;
+            tc = 0;
+        }
+        if (a.valid) {
+            bool any = false;  // a query block wholly in the padding has no row to write
+            for (int u = 0; u < BS / 32; ++u)
+                any = any || __ldg(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + qb * (BS / 32) + u) != 0;
+            if (!any) w.count = 0;
+        }
+    }
+    if constexpr (!WINDOW) w.n = (w.count + NSUB - 1) / NSUB;
+    const int n = w.n;
+
+    if (warp == 8) {
+        // ================= TMA producer =================
+        if (lane == 0 && n > 0) {
+            const CUtensorMap *mK = &maps.k[tc], *mV = &maps.v[tc];
+            tma_prefetch_desc(mK);
+            tma_prefetch_desc(mV);
+            mbar_arrive_expect_tx(q_full, 2 * BS * D * 2);
+            bwd_load_block<D, BS, TILED>(sQ, &maps.q[tc], q_full, qb, bh, a, tc);
+            bwd_load_block<D, BS, TILED>(sG, &maps.g[tc], q_full, qb, bh, a, tc);
+            bool ok = true;
+            int jk = 0, jv = 0;
+            for (int j = 0; j < n; ++j) {
+                const int ks = j % C::NK, vs = j % C::NV;
+                if (j >= C::NK && !mbar_wait(&k_empty[ks], ((j / C::NK) - 1) & 1, abort_flag)) { ok = false; break; }
+                mbar_arrive_expect_tx(&k_full[ks], C::TILE);
+                #pragma unroll
+                for (int u = 0; u < NSUB; ++u)
+                    bwd_load_block<D, BS, TILED>(sK + ks * C::TILE + u * BS * 128, mK, &k_full[ks],
+                                                 w.at(min(j * NSUB + u, w.count - 1)), bh, a, tc);
+                ++jk;
+                if (j >= C::NV && !mbar_wait(&v_empty[vs], ((j / C::NV) - 1) & 1, abort_flag)) { ok = false; break; }
+                mbar_arrive_expect_tx(&v_full[vs], C::TILE);
+                #pragma unroll
+                for (int u = 0; u < NSUB; ++u)
+                    bwd_load_block<D, BS, TILED>(sV + vs * C::TILE + u * BS * 128, mV, &v_full[vs],
+                                                 w.at(min(j * NSUB + u, w.count - 1)), bh, a, tc);
+                ++jv;
+            }
+            if (!ok) {
+                if (!*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
+                // let the loads already issued land before the CTA exits
+                mbar_wait(q_full, 0, nullptr);
+                for (int c = max(0, jk - C::NK); c < jk; ++c) mbar_wait(&k_full[c % C::NK], (c / C::NK) & 1, nullptr);
+                for (int c = max(0, jv - C::NV); c < jv; ++c) mbar_wait(&v_full[c % C::NV], (c / C::NV) & 1, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ================= MMA issuer =================
+        //   S(0) dP(0) S(1) | per tile j, once dX(j) is written: dQ(j) dP(j+1) S(j+2)
+        // S(j+2) overwrites the dX(j) that dQ(j) reads and waits for it to
+        // complete, with dP(j+1) in the pipe meanwhile.
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+            constexpr uint32_t idesc_d = idesc_bf16_f32(128, D, true);
+            const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
+            const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
+            const uint64_t dKt = sdesc_sw128(smem_u32(sK), SLAB, 1024);
+            constexpr uint64_t kTile16 = C::TILE >> 4;
+            bool ok = true;
+            auto score = [&](uint64_t A, uint64_t B, uint32_t d) {
+                #pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4);
+                    umma_bf16(tmem + d, A + off, B + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+            };
+            auto s_tile = [&](int j) -> bool {
+                if (!mbar_wait(&k_full[j % C::NK], (j / C::NK) & 1, abort_flag)) return false;
+                if (j >= 2 && !mbar_wait(dq_done, (j - 2) & 1, abort_flag)) return false;
+                tc_fence_after();
+                score(dQ, dK + (j % C::NK) * kTile16, (j & 1) * 128);
+                umma_commit(&s_full[j & 1]);
+                return true;
+            };
+            auto dp_tile = [&](int j) -> bool {
+                if (!mbar_wait(&v_full[j % C::NV], (j / C::NV) & 1, abort_flag)) return false;
+                tc_fence_after();
+                score(dG, dV + (j % C::NV) * kTile16, C::DP_COL);
+                umma_commit(dp_full);
+                umma_commit(&v_empty[j % C::NV]);
+                return true;
+            };
+            if (n > 0) {
+                ok = mbar_wait(q_full, 0, abort_flag) && s_tile(0) && dp_tile(0) && (n < 2 || s_tile(1));
+                for (int j = 0; ok && j < n; ++j) {
+                    if (!(ok = mbar_wait(ds_full, j & 1, abort_flag))) break;
+                    tc_fence_after();
+                    const uint32_t A = tmem + (j & 1) * 128;
+                    #pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16_ts(tmem + C::DQ_COL, A + (kk >> 2) * 64 + (kk & 3) * 8,
+                                     dKt + (j % C::NK) * kTile16 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_d,
+                                     (kk > 0 || j > 0) ? 1u : 0u);
+                    umma_commit(dq_done);
+                    umma_commit(&k_empty[j % C::NK]);
+                    if (j + 1 < n) ok = dp_tile(j + 1);
+                    if (ok && j + 2 < n) ok = s_tile(j + 2);
+                }
+                if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
+            }
+            umma_commit(mma_done);
+            mbar_wait(mma_done, 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ================= element-wise work (warps 0-7) =================
+        // warp w: TMEM lanes (query rows) 32 (w % 4) .., columns (keys) 64 (w / 4) ..
+        const int wq = warp & 3, hf = warp >> 2;
+        const int row = wq * 32 + lane;
+        const int p = qb * BS + row;          // this row's query position
+        const bool rows_live = wq * 32 < BS;  // warp-uniform
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const float sl2 = a.scale_log2;
+        float nl = -INFINITY, nd = 0.f;
+        if (row < BS && p < a.Pw) {
+            nl = __ldg(a.nlse + static_cast<size_t>(bh) * a.Pw + p);
+            nd = __ldg(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
+        }
+        [[maybe_unused]] float *part = nullptr;
+        [[maybe_unused]] float run_sum = 0.f;
+        [[maybe_unused]] int run_bucket = -1;
+        if constexpr (BIAS) {
+            if (a.dbias_part) {  // null: the table's gradient is not asked for
+                part = a.dbias_part + ((static_cast<size_t>(bh) * a.nt + qb) * 8 + warp) * a.buckets;
+                for (int b = lane; b < a.buckets; b += 32) part[b] = 0.f;
+                __syncwarp();
+            }
+        }
+        // the warp's sum of the current bucket's row sums goes to its partial
+        auto flush = [&]() {
+            if constexpr (BIAS) {
+                float s = run_sum;
+                #pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0 && part && run_bucket >= 0) part[run_bucket] += s;
+                __syncwarp();
+                run_sum = 0.f;
+            }
+        };
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            // which of the 64 columns this row sees
+            uint32_t see[2] = {~0u, ~0u};
+            bool masked = false;
+            if (rows_live) {
+                if constexpr (WINDOW) {
+                    const int q0 = qb * 128, ks = w.at(j) * 128;
+                    masked = !((ks + 128 <= a.P) && (a.dense || ks + 128 <= a.sink ||
+                                                     max(min(q0 + 128, a.P) - 1 - ks, ks + 127 - q0) <= a.half));
+                    if (masked) {
+                        #pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int c = ks + 64 * hf + 32 * u;
+                            see[u] = a.dense ? ~0u : span_bits(c, p - a.half, p + a.half + 1) | span_bits(c, 0, a.sink);
+                            see[u] &= span_bits(c, 0, a.P);
+                        }
+                    }
+                } else {
+                    if (a.group > 0 || a.gstride > 1 || a.valid || w.count % NSUB != 0) {
+                        masked = true;
+                        #pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int c = 64 * hf + 32 * u, x = j * NSUB + c / BS;
+                            const int kc = w.at(min(x, w.count - 1)) * BS + c % BS;
+                            if (a.group > 0 || a.gstride > 1) see[u] = group_bits(a, p, kc);
+                            if (a.valid) see[u] &= __ldg(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + kc / 32);
+                            if (x >= w.count) see[u] = 0u;  // past the list's end: its last block again
+                        }
+                    }
+                }
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            float pr[64];
+            [[maybe_unused]] bool uniform = true;
+            [[maybe_unused]] int bucket = 0, diag0 = 0;
+            if (rows_live) {
+                uint32_t x[64];
+                tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                float y0 = nl;
+                [[maybe_unused]] BiasPiece piece[2];
+                if constexpr (BIAS) {
+                    const float *E = a.E + static_cast<size_t>(bh % a.H) * (2 * a.R + 1) + a.R;
+                    const int d = (w.at(j) - qb) * 128;
+                    uniform = bias_uniform(a.bm + a.R, a.R, d, bucket);
+                    diag0 = d + 64 * hf - wq * 32;  // offset of (row lane 0, column 64 hf)
+                    if (uniform) {
+                        y0 += __ldg(E + min(max(d, -a.R), a.R));
+                    } else {
+                        piece[0] = bias_piece(E, a.R, 1, diag0, lane);
+                        piece[1] = bias_piece(E, a.R, 1, diag0 + 32, lane);
+                    }
+                }
+                tmem_ld_wait();
+                const uint64_t sl2x2 = f32x2(sl2, sl2), y0x2 = f32x2(y0, y0);
+                #pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    float y[2];
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, y0x2), y[0], y[1]);
+                    if constexpr (BIAS) {
+                        if (!uniform) {
+                            y[0] += bias_at(piece[c >> 5], c & 31, lane);
+                            y[1] += bias_at(piece[c >> 5], (c + 1) & 31, lane);
+                        }
+                    }
+                    if (masked) {
+                        if (!((see[c >> 5] >> (c & 31)) & 1u)) y[0] = -INFINITY;
+                        if (!((see[c >> 5] >> ((c + 1) & 31)) & 1u)) y[1] = -INFINITY;
+                    }
+                    pr[c] = ex2_approx(y[0]);
+                    pr[c + 1] = ex2_approx(y[1]);
+                }
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            if (rows_live) {
+                uint32_t dsk[32];
+                const uint64_t ndx2 = f32x2(nd, nd);
+                #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t x[32];
+                    tmem_ld32(t_lane + C::DP_COL + 64 * hf + 32 * u, x);
+                    tmem_ld_wait();
+                    #pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        float &d0 = pr[32 * u + c], &d1 = pr[32 * u + c + 1];
+                        f32x2_split(mul_f32x2(f32x2(d0, d1),
+                                              add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), ndx2)),
+                                    d0, d1);
+                        dsk[16 * u + (c >> 1)] = pack_bf16x2(d0, d1);  // bf16: the type of the MMA's operand
+                    }
+                }
+                tmem_st32(t_lane + (j & 1) * 128 + 64 * hf, dsk);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ds_full);
+            if constexpr (BIAS) {
+                // sums of the unrounded dX (in pr) by bucket, after the MMA has its operand
+                if (!part) {
+                } else if (uniform) {
+                    if (bucket != run_bucket) {
+                        flush();
+                        run_bucket = bucket;
+                    }
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    #pragma unroll
+                    for (int c = 0; c < 64; ++c) s[c & 3] += pr[c];
+                    run_sum += (s[0] + s[1]) + (s[2] + s[3]);
+                } else {
+                    // diag[m]: the sum of the diagonal at offset diag0 + 32 (m - 1) + lane
+                    float diag[3] = {0.f, 0.f, 0.f};
+                    #pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float v = __shfl_sync(0xffffffffu, pr[32 * u + i], (i - lane) & 31);
+                            if (i >= lane) diag[u + 1] += v;
+                            else diag[u] += v;
+                        }
+                    #pragma unroll
+                    for (int m = 0; m < 3; ++m) {
+                        // offsets rise with the lane, so equal buckets are neighbours:
+                        // sum each run, its last lane adds to the warp's partial
+                        const int o = diag0 + 32 * (m - 1) + lane;
+                        const int b = __ldg(a.bm + a.R + min(max(o, -a.R), a.R));
+                        float v = diag[m];
+                        #pragma unroll
+                        for (int s = 1; s < 32; s <<= 1) {
+                            const float t = __shfl_up_sync(0xffffffffu, v, s);
+                            const int tb = __shfl_up_sync(0xffffffffu, b, s);
+                            if (lane >= s && tb == b) v += t;
+                        }
+                        const int nb = __shfl_down_sync(0xffffffffu, b, 1);
+                        if (lane == 31 || nb != b) part[b] += v;
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
+        flush();
+
+        // ---- epilogue: warps 0-3 write the first half of the columns, 4-7 the second ----
+        const int r = rows_live && row < BS && head_ok ? bwd_row_of<TILED>(p, a, tc) : -1;
+        const size_t at = (static_cast<size_t>(bh) * a.S_out + max(r, 0)) * D;
+        if (ok && n > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait(dq_done, (n - 1) & 1, abort_flag))) {
+                if (!*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
+            } else if (rows_live) {
+                tc_fence_after();
+                #pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t x[32];
+                    const int col = hf * (D / 2) + 32 * c;
+                    tmem_ld32(t_lane + C::DQ_COL + col, x);
+                    tmem_ld_wait();
+                    if (r >= 0) bwd_store32(x, a.scale, a.d0, a.out_f32, at + col);
+                }
+            }
+        } else if (n == 0 && r >= 0 && hf == 0) {
+            bwd_zero_row(a.d0, a.out_f32, at, D);  // an invalid list
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
+vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
+    using C = DqCfg<D>;
+    auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention backward, dQ)");
+    dim3 grid(a.nt, a.BH);
+    kern<<<grid, kBwdThreads, C::SMEM, st>>>(maps, a);
+    return check_cuda(cudaGetLastError(), "attention backward launch (dQ)");
+}
+
+template <int D>
+vsa_status pick(const BwdMaps &maps, const BwdArgs &a, int block, bool window, bool tiled, bool bias, cudaStream_t st) {
+    if (window) return bias ? run<D, 128, true, false, true>(maps, a, st) : run<D, 128, true, false, false>(maps, a, st);
+    if (tiled) {
+        if (block == 128) return run<D, 128, false, true, false>(maps, a, st);
+        return block == 64 ? run<D, 64, false, true, false>(maps, a, st) : run<D, 32, false, true, false>(maps, a, st);
+    }
+    if (block == 128) return run<D, 128, false, false, false>(maps, a, st);
+    return block == 64 ? run<D, 64, false, false, false>(maps, a, st) : run<D, 32, false, false, false>(maps, a, st);
+}
+
+}  // namespace
+
+vsa_status launch_bwd_dq(const BwdMaps &maps, const BwdArgs &a, int D, int block, bool window, bool tiled, bool bias,
+                         cudaStream_t st) {
+    return D == 128 ? pick<128>(maps, a, block, window, tiled, bias, st) : pick<64>(maps, a, block, window, tiled, bias, st);
+}
+
+}  // namespace vsa

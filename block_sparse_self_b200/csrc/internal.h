@@ -105,6 +105,13 @@ struct AttnLaunch {
     // the softmax state behind the normalised output, in the log2 domain:
     // (m, l) with l = sum over the visible keys of 2^(scale log2e q.k - m)
     float2 *stats;
+    // optional: per row of o (row r of head bh at lse[bh * S + r]) the natural
+    // logarithm of the sum behind its softmax, -inf where no key was seen
+    float *lse;
+    // window mode, optional: relative position bias by offset (relative_bias.cu)
+    const float *bias_E;
+    const uint8_t *bias_bm;
+    int bias_R, n_heads;
 };
 vsa_status launch_attention(const AttnLaunch &a, int *status, cudaStream_t st);
 // Two query tiles per CTA (128-token blocks only); launch_attention routes to it.
@@ -132,6 +139,39 @@ cudaError_t launch_head_profile(const void *q, const void *k, int BH, int S, int
 // Skipped key blocks compensated by their centroids (compensated.cu).
 size_t compensated_workspace_bytes(int BH, int S, int D, int out_f32);
 vsa_status launch_compensated(const AttnLaunch &a, void *workspace, int *status, cudaStream_t st);
+
+// Block lists turned round (transpose_lists.cu): offsets [lists, nb + 1] and
+// rows [lists, nb * cap]; `fill` writes -1 behind each list's last entry.
+size_t transpose_lists_workspace_bytes(int lists, int nb);
+cudaError_t launch_transpose_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap, int32_t *offsets,
+                                   int32_t *rows, bool fill, void *workspace, int *status, cudaStream_t st);
+
+// Relative position bias (relative_bias.cu): values by offset -R .. R, R =
+// bias_reach(S, far), in the workspace; bucket numbers; the gradient's last sum.
+int bias_reach(int S, int far);
+size_t bias_workspace_bytes(int H, int S, int far);
+cudaError_t launch_bias_expand(const void *table, bool f32, int H, int S, int buckets, int far, void *workspace,
+                               const float **E, const uint8_t **bm, cudaStream_t st);
+cudaError_t launch_bias_buckets(int buckets, int far, int32_t *out, cudaStream_t st);
+cudaError_t launch_dbias(const float *part, int B, int H, int per, int buckets, void *dtable, bool f32,
+                         cudaStream_t st);
+
+// The attention's backward pass (backward.cu): `a` as for the forward pass
+// (o, out_f32 and stats unused).
+struct BackwardLaunch {
+    AttnLaunch a;
+    const void *g, *o;   // dL/do (bf16) and the forward output
+    int o_f32;
+    const float *lse;
+    void *dq, *dk, *dv;
+    int grad_f32;
+    int H;               // heads (a.BH = batch * H)
+    const void *bias;    // window mode: table [buckets, H] or nullptr
+    int bias_f32, buckets, far;
+    void *dbias;         // its gradient in the table's type, or nullptr
+};
+size_t backward_workspace_bytes(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far);
+vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status, cudaStream_t st);
 
 // Address and size of the file-scope scratch array that
 // vsa_select_tiling_noalloc uses (see cached_symbol_address).

@@ -1,0 +1,130 @@
+// relative_bias.cu -- the learned relative position bias of window attention:
+// its buckets, its values by offset, and the last step of its gradient.
+//
+// A pair (query i, key j) of head h gets table[bucket(j - i)][h] added to its
+// scaled logit.  With n = buckets / 2, e = n / 2 (rounded down) and
+//   f(d) = d for d < e, else min(n - 1, e + floor((n - e) ln(d / e) / ln(far / e))),
+// bucket(r) = f(|r|) + (n if r > 0).  f steps up where d reaches
+// e (far / e)^(t / (n - e)); those borders are rounded up to whole numbers on
+// the host, so the kernels only compare integers.
+//
+// The attention kernels read the bias by offset: E[h][r + R] = log2(e)
+// table[bucket(r)][h] for |r| <= R, R = min(far, S) (larger offsets fall into
+// the last bucket of their side).  E is a few KB to a few MB and stays in L2.
+#include "common.cuh"
+#include "internal.h"
+
+namespace vsa {
+
+namespace {
+
+struct Borders {
+    int e, n, steps;   // f(d) = d below e; then e + the borders that d has reached
+    int at[128];
+};
+
+Borders make_borders(int buckets, int far) {
+    Borders b{};
+    b.n = buckets / 2;
+    b.e = b.n / 2;
+    const int m = b.n - b.e;
+    for (int t = 1; t < m; ++t) {
+        // a border that is a whole number must not be rounded up to the next
+        const long double x = static_cast<long double>(b.e) *
+                              powl(static_cast<long double>(far) / b.e, static_cast<long double>(t) / m);
+        b.at[b.steps++] = static_cast<int>(ceill(x * (1.0L - 1e-13L)));
+    }
+    return b;
+}
+
+__device__ __forceinline__ int bucket_of(int r, const Borders &b) {
+    const int d = r < 0 ? -r : r;
+    int f = d;
+    if (d >= b.e) {
+        f = b.e;
+        for (int t = 0; t < b.steps; ++t) f += d >= b.at[t];
+    }
+    return f + (r > 0 ? b.n : 0);
+}
+
+__global__ void buckets_kernel(const Borders b, int far, int32_t *__restrict__ out) {
+    const int x = blockIdx.x * 256 + threadIdx.x;
+    if (x <= 2 * far) out[x] = bucket_of(x - far, b);
+}
+
+template <typename T>
+__global__ void expand_kernel(const Borders b, const T *__restrict__ table, int H, int R, float *__restrict__ E,
+                              uint8_t *__restrict__ bm) {
+    const int x = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
+    if (x > 2 * R) return;
+    const int k = bucket_of(x - R, b);
+    E[static_cast<size_t>(h) * (2 * R + 1) + x] =
+        static_cast<float>(table[static_cast<size_t>(k) * H + h]) * 1.4426950408889634f;
+    if (h == 0) bm[x] = static_cast<uint8_t>(k);
+}
+
+// dtable[b][h]: the partial sums [B, H, per, buckets] over the batch and the
+// warps of every query tile, in a fixed order and in 64 bits.
+template <typename T>
+__global__ void __launch_bounds__(1024) dbias_kernel(const float *__restrict__ part, int B, int H, int per, int buckets,
+                                                     T *__restrict__ dtable) {
+    __shared__ double sum[32][33];
+    const int b = blockIdx.x * 32 + threadIdx.x, h = blockIdx.y;
+    double s = 0.0;
+    if (b < buckets)
+        for (int i = threadIdx.y; i < B * per; i += 32) {
+            const int n = i / per;
+            s += part[((static_cast<size_t>(n) * H + h) * per + (i - n * per)) * buckets + b];
+        }
+    sum[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && b < buckets) {
+        for (int y = 1; y < 32; ++y) s += sum[y][threadIdx.x];
+        dtable[static_cast<size_t>(b) * H + h] = static_cast<T>(static_cast<float>(s));
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+int bias_reach(int S, int far) { return far < S ? far : S; }
+
+size_t bias_workspace_bytes(int H, int S, int far) {
+    const size_t n = 2 * static_cast<size_t>(bias_reach(S, far)) + 1;
+    return up256(static_cast<size_t>(H) * n * 4) + up256(n);
+}
+
+cudaError_t launch_bias_expand(const void *table, bool f32, int H, int S, int buckets, int far, void *workspace,
+                               const float **E, const uint8_t **bm, cudaStream_t st) {
+    const int R = bias_reach(S, far);
+    const size_t n = 2 * static_cast<size_t>(R) + 1;
+    float *e = static_cast<float *>(workspace);
+    uint8_t *m = static_cast<uint8_t *>(workspace) + up256(static_cast<size_t>(H) * n * 4);
+    const Borders b = make_borders(buckets, far);
+    const dim3 grid(static_cast<unsigned>((n + 255) / 256), H);
+    if (f32)
+        expand_kernel<<<grid, 256, 0, st>>>(b, static_cast<const float *>(table), H, R, e, m);
+    else
+        expand_kernel<<<grid, 256, 0, st>>>(b, static_cast<const __nv_bfloat16 *>(table), H, R, e, m);
+    *E = e;
+    *bm = m;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bias_buckets(int buckets, int far, int32_t *out, cudaStream_t st) {
+    buckets_kernel<<<(2 * far + 256) / 256, 256, 0, st>>>(make_borders(buckets, far), far, out);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dbias(const float *part, int B, int H, int per, int buckets, void *dtable, bool f32,
+                         cudaStream_t st) {
+    const dim3 grid((buckets + 31) / 32, H), block(32, 32);
+    if (f32)
+        dbias_kernel<<<grid, block, 0, st>>>(part, B, H, per, buckets, static_cast<float *>(dtable));
+    else
+        dbias_kernel<<<grid, block, 0, st>>>(part, B, H, per, buckets, static_cast<__nv_bfloat16 *>(dtable));
+    return cudaGetLastError();
+}
+
+}  // namespace vsa

@@ -464,6 +464,110 @@ vsa_status vsa_head_profile(const void *q, const void *k, int B, int n_heads, in
                             size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Training: the attention calls' backward passes.
+ *
+ * The forward calls with _lse in their names are the calls above with one
+ * more output, lse [B, n_heads, S] fp32: per row of o the natural logarithm
+ * of the sum behind its softmax (-inf for a row that saw no key, whose o is
+ * zero).  o is the same bit for bit.
+ *
+ * With x_ij = scale q_i . k_j (+ bias) over the keys row i sees,
+ * P_ij = exp(x_ij - lse_i), g = dL/do and delta_i = g_i . o_i:
+ *   dv_j = sum_i P_ij g_i,    dx_ij = P_ij (g_i . v_j - delta_i),
+ *   dq_i = scale sum_j dx_ij k_j,   dk_j = scale sum_i dx_ij q_i.
+ * P is recomputed from q, k and lse.  Products run in bf16 with fp32
+ * accumulation (P and dx enter them rounded to bf16), everything else in
+ * fp32; every sum has one order, so gradients repeat bit for bit.  Rows that
+ * saw no key, and rows whose list is invalid, pass no gradient; keys that no
+ * row sees get zeros.  As in the forward pass a masked pair inside a block
+ * that is computed has weight zero, and zero times a non-finite q, k, v or
+ * dout of that block is NaN; blocks that no list names are not read.
+ *   dout       [B, n_heads, S, D] bf16, in the order of o
+ *   o, lse     as the forward call wrote them, o in o_dtype
+ *   dq, dk, dv [B, n_heads, S, D] in grad_dtype, in the order of q, k and v
+ *   workspace  DEVICE scratch of the _workspace_size call's bytes, 256-byte
+ *              aligned, one per call in flight
+ * Outputs and workspace must not overlap one another or an input.  All other
+ * arguments as in the forward call.                                         */
+vsa_status vsa_block_sparse_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
+                                          float *lse, int B, int n_heads, int S, int D, int block, const int32_t *idx,
+                                          const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
+                                          void *stream);
+vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, const void *v, void *o,
+                                                vsa_dtype out_dtype, float *lse, int B, int n_heads, int S, int D,
+                                                vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
+                                                const int32_t *choice, const int32_t *idx, const int32_t *cnt, int cap,
+                                                int list_per_head, int group_stride, float scale, void *stream);
+
+/* positions: S, or the tokens of vsa_padded_grid in tiled mode (block then
+ * min(tile volume, 128)).  0 for invalid arguments.                         */
+size_t vsa_block_sparse_attention_backward_workspace_size(int B, int n_heads, int positions, int block, int cap,
+                                                          int list_per_head);
+vsa_status vsa_block_sparse_attention_backward(const void *dout, const void *q, const void *k, const void *v,
+                                               const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+                                               void *dv, vsa_dtype grad_dtype, int B, int n_heads, int S, int D,
+                                               int block, const int32_t *idx, const int32_t *cnt, int cap,
+                                               int list_per_head, int group_size, float scale, void *workspace,
+                                               size_t workspace_bytes, void *stream);
+vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const void *q, const void *k, const void *v,
+                                                     const void *o, vsa_dtype o_dtype, const float *lse, void *dq,
+                                                     void *dk, void *dv, vsa_dtype grad_dtype, int B, int n_heads,
+                                                     int S, int D, vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
+                                                     const int32_t *choice, const int32_t *idx, const int32_t *cnt,
+                                                     int cap, int list_per_head, int group_stride, float scale,
+                                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Window attention with an optional learned relative position bias: the
+ * logit of query i and key j of head h becomes
+ *   scale q_i . k_j + bias[bucket(j - i)][h].
+ * With n = num_buckets / 2, e = n / 2 (rounded down) and
+ *   f(d) = d for d < e, else min(n - 1, e + floor((n - e) ln(d / e) / ln(max_distance / e))),
+ * bucket(r) = f(|r|) + (n if r > 0): short distances have a bucket each,
+ * longer ones share buckets that widen with the distance, and everything from
+ * max_distance on is in the last one.
+ *   lse        output as above, or NULL
+ *   bias       [num_buckets, n_heads] in bias_dtype, or NULL (num_buckets and
+ *              max_distance are then ignored and workspace may be NULL)
+ *   num_buckets even, in [4, 256]; max_distance in (num_buckets / 4, 2^24]
+ *   dbias      [num_buckets, n_heads] in bias_dtype, or NULL: the gradient,
+ *              dbias[b][h] = sum over the batch and the visible pairs whose
+ *              offset is in bucket b of dx_ij (fp32 from unrounded dx, the
+ *              last sum in 64 bits)
+ *   workspace  DEVICE scratch of vsa_window_attention_lse_workspace_size
+ *              (0 without a bias: num_buckets = 0) or, for the backward pass,
+ *              vsa_window_attention_backward_workspace_size bytes             */
+size_t vsa_window_attention_lse_workspace_size(int n_heads, int S, int num_buckets, int max_distance);
+vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
+                                    float *lse, int B, int n_heads, int S, int D, int window, int sink, float scale,
+                                    const void *bias, vsa_dtype bias_dtype, int num_buckets, int max_distance,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+size_t vsa_window_attention_backward_workspace_size(int B, int n_heads, int S, int num_buckets, int max_distance);
+vsa_status vsa_window_attention_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
+                                         vsa_dtype o_dtype, const float *lse, void *dq, void *dk, void *dv,
+                                         vsa_dtype grad_dtype, int B, int n_heads, int S, int D, int window, int sink,
+                                         float scale, const void *bias, vsa_dtype bias_dtype, int num_buckets,
+                                         int max_distance, void *dbias, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* out[r + max_distance] = bucket(r) for |r| <= max_distance (int32).        */
+vsa_status vsa_relative_position_buckets(int num_buckets, int max_distance, int32_t *out, void *stream);
+
+/* Block lists turned round: for each key block the query blocks that list
+ * it, ascending.  The backward passes build the same lists in their
+ * workspace; this call is for callers that walk key blocks themselves.
+ *   idx, cnt  [lists, nb, cap], [lists, nb] as the list calls write them
+ *             (strictly ascending entries in [0, nb), 0 <= cnt <= cap)
+ *   offsets   [lists, nb + 1]: key block j's query blocks are
+ *             rows[offsets[j] .. offsets[j + 1])
+ *   rows      [lists, nb * cap], -1 behind the last entry
+ * A query block whose list breaks these rules appears nowhere and sets
+ * VSA_ERR_RUNTIME.  nb * cap < 2^31.                                        */
+size_t vsa_transpose_block_lists_workspace_size(int lists, int nb);
+vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap,
+                                     int32_t *offsets, int32_t *rows, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* The whole SPADE path for Q, K, V and O in HOST memory.  "Adaptive tiling
  * (SPADE)", Recipe: per (b, head) the tiling choice (skipped with one
  * candidate), the tile-contiguous order, the min/max block scores, the top-k
