@@ -274,7 +274,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
         __syncwarp();
     } else if (warp == 5) {
         // ================= MMA issuer =================
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
             const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV), aP = smem_u32(sP);

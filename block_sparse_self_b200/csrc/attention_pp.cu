@@ -340,7 +340,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         __syncwarp();
     } else if (warp == 9) {
         // ================= MMA issuer =================
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
             // Descriptor bases, built once.  The start-address field holds
@@ -912,7 +912,7 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     } else if (warp == 5) {
         // ================= MMA issuer =================
         // per tile w: [wait PV(w-1)] QK(w) | [wait P(w), V(w), O read out of w-1] PV(w)
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, BN, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
             // descriptor bases (start-address field addr >> 4; every address here

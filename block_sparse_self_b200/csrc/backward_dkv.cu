@@ -185,65 +185,69 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
         // S(j+1) overwrites the P(j) that dV(j) reads and dP(j+1) the dX(j)
         // that dK(j) reads; an MMA only orders behind an earlier one with the
         // same accumulator, so each waits for the reader to complete.
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
             constexpr uint32_t idesc_d = idesc_bf16_f32(128, D, true);
+            // the CTA holds all of tensor memory, so it starts at column 0
+            constexpr uint32_t tm = 0;
             const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
             const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
             const uint64_t dQt = sdesc_sw128(smem_u32(sQ), SLAB, 1024), dGt = sdesc_sw128(smem_u32(sG), SLAB, 1024);
-            constexpr uint64_t kTile16 = C::TILE >> 4;
+            constexpr uint64_t kT = C::TILE >> 4;
             bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag); };
             auto score = [&](uint64_t A, uint64_t B, uint32_t d, uint64_t *bar) {
                 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4);
-                    umma_bf16(tmem + d, A + off, B + off, idesc_s, kk > 0 ? 1u : 0u);
+                    umma_bf16(tm + d, A + off, B + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(bar);
             };
             auto accum = [&](uint32_t A, uint64_t B, uint32_t d, bool first) {
                 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    umma_bf16_ts(tmem + d, tmem + A + (kk >> 2) * 64 + (kk & 3) * 8,
+                    umma_bf16_ts(tm + d, tm + A + (kk >> 2) * 64 + (kk & 3) * 8,
                                  B + static_cast<uint64_t>((kk * 2048) >> 4), idesc_d, (kk > 0 || !first) ? 1u : 0u);
             };
             if (n > 0) {
-                ok = mbar_wait(kv_full, 0, abort_flag) && mbar_wait(&q_full[0], 0, abort_flag);
+                ok = wait(kv_full, 0) && wait(&q_full[0], 0);
                 if (ok) {
                     tc_fence_after();
                     score(dK, dQ, C::S_COL, s_full);
-                    ok = mbar_wait(&g_full[0], 0, abort_flag);
+                    ok = wait(&g_full[0], 0);
                 }
                 if (ok) {
                     tc_fence_after();
                     score(dV, dG, C::DP_COL, dp_full);
                 }
+                // ring positions of tiles j (qs, gs) and j + 1 (qn, gn, with their parities)
+                int qs = 0, gs = 0, qn = 1, gn = 1, qp = 0, gp = 0;
                 for (int j = 0; ok && j < n; ++j) {
-                    const int qs = j % C::NQ, gs = j % C::NG, qn = (j + 1) % C::NQ, gn = (j + 1) % C::NG;
-                    if (!(ok = mbar_wait(p_full, j & 1, abort_flag))) break;
+                    if (!(ok = wait(p_full, j & 1))) break;
                     tc_fence_after();
-                    accum(C::S_COL, dGt + gs * kTile16, C::DV_COL, j == 0);
+                    accum(C::S_COL, dGt + gs * kT, C::DV_COL, j == 0);
                     umma_commit(dv_done);
                     umma_commit(&g_empty[gs]);
                     if (j + 1 < n) {
-                        if (!(ok = mbar_wait(&q_full[qn], ((j + 1) / C::NQ) & 1, abort_flag) &&
-                                   mbar_wait(dv_done, j & 1, abort_flag)))
-                            break;
+                        if (!(ok = wait(&q_full[qn], qp) && wait(dv_done, j & 1))) break;
                         tc_fence_after();
-                        score(dK, dQ + qn * kTile16, C::S_COL, s_full);
+                        score(dK, dQ + qn * kT, C::S_COL, s_full);
                     }
-                    if (!(ok = mbar_wait(ds_full, j & 1, abort_flag))) break;
+                    if (!(ok = wait(ds_full, j & 1))) break;
                     tc_fence_after();
-                    accum(C::DP_COL, dQt + qs * kTile16, C::DK_COL, j == 0);
+                    accum(C::DP_COL, dQt + qs * kT, C::DK_COL, j == 0);
                     umma_commit(dk_done);
                     umma_commit(&q_empty[qs]);
                     if (j + 1 < n) {
-                        if (!(ok = mbar_wait(&g_full[gn], ((j + 1) / C::NG) & 1, abort_flag) &&
-                                   mbar_wait(dk_done, j & 1, abort_flag)))
-                            break;
+                        if (!(ok = wait(&g_full[gn], gp) && wait(dk_done, j & 1))) break;
                         tc_fence_after();
-                        score(dV, dG + gn * kTile16, C::DP_COL, dp_full);
+                        score(dV, dG + gn * kT, C::DP_COL, dp_full);
                     }
+                    qs = qn;
+                    gs = gn;
+                    if (++qn == C::NQ) { qn = 0; qp ^= 1; }
+                    if (++gn == C::NG) { gn = 0; gp ^= 1; }
                 }
                 if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
             }
@@ -313,34 +317,42 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                     }
                 }
                 tmem_ld_wait();
+                // the exponents, in place; the mask is one branch after all of them, so
+                // that the exponentials below are one straight run
                 const uint64_t sl2x2 = f32x2(sl2, sl2);
                 #pragma unroll
                 for (int c4 = 0; c4 < 16; ++c4) {
                     const float4 l4 = nl[c4];
-                    float y[4];
+                    float y0, y1, y2, y3;
+                    uint64_t b0 = f32x2(l4.x, l4.y), b1 = f32x2(l4.z, l4.w);
                     if constexpr (BIAS) {
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = 4 * c4 + e;
-                            const float b = uniform ? flat : bias_at(piece[c >> 5], c & 31, lane);
-                            y[e] = fmaf(__uint_as_float(x[c]), sl2, b) + (&l4.x)[e];
-                        }
-                    } else {
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4]), __uint_as_float(x[4 * c4 + 1])), sl2x2,
-                                              f32x2(l4.x, l4.y)),
-                                    y[0], y[1]);
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4 + 2]), __uint_as_float(x[4 * c4 + 3])),
-                                              sl2x2, f32x2(l4.z, l4.w)),
-                                    y[2], y[3]);
+                        b0 = add_f32x2(b0, f32x2(flat, flat));
+                        b1 = add_f32x2(b1, f32x2(flat, flat));
                     }
-                    if (masked) {
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!((see[c4 >> 3] >> ((4 * c4 + e) & 31)) & 1u)) y[e] = -INFINITY;
-                    }
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) pr[4 * c4 + e] = ex2_approx(y[e]);
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4]), __uint_as_float(x[4 * c4 + 1])), sl2x2, b0),
+                                y0, y1);
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4 + 2]), __uint_as_float(x[4 * c4 + 3])), sl2x2,
+                                          b1),
+                                y2, y3);
+                    x[4 * c4] = __float_as_uint(y0);
+                    x[4 * c4 + 1] = __float_as_uint(y1);
+                    x[4 * c4 + 2] = __float_as_uint(y2);
+                    x[4 * c4 + 3] = __float_as_uint(y3);
                 }
+                if constexpr (BIAS) {
+                    if (!uniform) {
+                        #pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(piece[c >> 5], c & 31, lane));
+                    }
+                }
+                if (masked) {
+                    #pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (!((see[c >> 5] >> (c & 31)) & 1u)) x[c] = 0xff800000u;  // -inf
+                }
+                #pragma unroll
+                for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(__uint_as_float(x[c]));
                 // P enters dV rounded to bf16 (the MMA's operand type); dX below
                 // uses it unrounded, so it is rounded once on its way to dK
                 uint32_t pk[32];

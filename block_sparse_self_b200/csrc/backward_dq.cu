@@ -200,51 +200,59 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
         //   S(0) dP(0) S(1) | per tile j, once dX(j) is written: dQ(j) dP(j+1) S(j+2)
         // S(j+2) overwrites the dX(j) that dQ(j) reads and waits for it to
         // complete, with dP(j+1) in the pipe meanwhile.
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
             constexpr uint32_t idesc_d = idesc_bf16_f32(128, D, true);
+            // the CTA holds all of tensor memory, so it starts at column 0
+            constexpr uint32_t tm = 0;
             const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
             const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
             const uint64_t dKt = sdesc_sw128(smem_u32(sK), SLAB, 1024);
-            constexpr uint64_t kTile16 = C::TILE >> 4;
+            constexpr uint64_t kT = C::TILE >> 4;
             bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag); };
             auto score = [&](uint64_t A, uint64_t B, uint32_t d) {
                 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t off = static_cast<uint64_t>(((kk >> 2) * SLAB + (kk & 3) * 32) >> 4);
-                    umma_bf16(tmem + d, A + off, B + off, idesc_s, kk > 0 ? 1u : 0u);
+                    umma_bf16(tm + d, A + off, B + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
             };
+            // ring positions, advanced without divisions
+            int ks = 0, kp = 0, vs = 0, vp = 0, kd = 0;
             auto s_tile = [&](int j) -> bool {
-                if (!mbar_wait(&k_full[j % C::NK], (j / C::NK) & 1, abort_flag)) return false;
-                if (j >= 2 && !mbar_wait(dq_done, (j - 2) & 1, abort_flag)) return false;
+                if (!wait(&k_full[ks], kp)) return false;
+                if (j >= 2 && !wait(dq_done, (j - 2) & 1)) return false;
                 tc_fence_after();
-                score(dQ, dK + (j % C::NK) * kTile16, (j & 1) * 128);
+                score(dQ, dK + ks * kT, (j & 1) * 128);
                 umma_commit(&s_full[j & 1]);
+                if (++ks == C::NK) { ks = 0; kp ^= 1; }
                 return true;
             };
-            auto dp_tile = [&](int j) -> bool {
-                if (!mbar_wait(&v_full[j % C::NV], (j / C::NV) & 1, abort_flag)) return false;
+            auto dp_tile = [&]() -> bool {
+                if (!wait(&v_full[vs], vp)) return false;
                 tc_fence_after();
-                score(dG, dV + (j % C::NV) * kTile16, C::DP_COL);
+                score(dG, dV + vs * kT, C::DP_COL);
                 umma_commit(dp_full);
-                umma_commit(&v_empty[j % C::NV]);
+                umma_commit(&v_empty[vs]);
+                if (++vs == C::NV) { vs = 0; vp ^= 1; }
                 return true;
             };
             if (n > 0) {
-                ok = mbar_wait(q_full, 0, abort_flag) && s_tile(0) && dp_tile(0) && (n < 2 || s_tile(1));
+                ok = wait(q_full, 0) && s_tile(0) && dp_tile() && (n < 2 || s_tile(1));
                 for (int j = 0; ok && j < n; ++j) {
-                    if (!(ok = mbar_wait(ds_full, j & 1, abort_flag))) break;
+                    if (!(ok = wait(ds_full, j & 1))) break;
                     tc_fence_after();
-                    const uint32_t A = tmem + (j & 1) * 128;
+                    const uint32_t A = tm + (j & 1) * 128;
                     #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16_ts(tmem + C::DQ_COL, A + (kk >> 2) * 64 + (kk & 3) * 8,
-                                     dKt + (j % C::NK) * kTile16 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_d,
+                        umma_bf16_ts(tm + C::DQ_COL, A + (kk >> 2) * 64 + (kk & 3) * 8,
+                                     dKt + kd * kT + static_cast<uint64_t>((kk * 2048) >> 4), idesc_d,
                                      (kk > 0 || j > 0) ? 1u : 0u);
                     umma_commit(dq_done);
-                    umma_commit(&k_empty[j % C::NK]);
-                    if (j + 1 < n) ok = dp_tile(j + 1);
+                    umma_commit(&k_empty[kd]);
+                    if (++kd == C::NK) kd = 0;
+                    if (j + 1 < n) ok = dp_tile();
                     if (ok && j + 2 < n) ok = s_tile(j + 2);
                 }
                 if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
@@ -345,23 +353,31 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
                 }
                 tmem_ld_wait();
                 const uint64_t sl2x2 = f32x2(sl2, sl2), y0x2 = f32x2(y0, y0);
+                // the exponents, in place; the mask is one branch after all of them, so
+                // that the exponentials below are one straight run
+                // the exponents, in place; the mask is one branch after all of them, so
+                // that the exponentials below are one straight run
                 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
                     float y[2];
                     f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, y0x2), y[0], y[1]);
-                    if constexpr (BIAS) {
-                        if (!uniform) {
-                            y[0] += bias_at(piece[c >> 5], c & 31, lane);
-                            y[1] += bias_at(piece[c >> 5], (c + 1) & 31, lane);
-                        }
-                    }
-                    if (masked) {
-                        if (!((see[c >> 5] >> (c & 31)) & 1u)) y[0] = -INFINITY;
-                        if (!((see[c >> 5] >> ((c + 1) & 31)) & 1u)) y[1] = -INFINITY;
-                    }
-                    pr[c] = ex2_approx(y[0]);
-                    pr[c + 1] = ex2_approx(y[1]);
+                    x[c] = __float_as_uint(y[0]);
+                    x[c + 1] = __float_as_uint(y[1]);
                 }
+                if constexpr (BIAS) {
+                    if (!uniform) {
+                        #pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(piece[c >> 5], c & 31, lane));
+                    }
+                }
+                if (masked) {
+                    #pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (!((see[c >> 5] >> (c & 31)) & 1u)) x[c] = 0xff800000u;  // -inf
+                }
+                #pragma unroll
+                for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(__uint_as_float(x[c]));
             }
             if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();

@@ -254,6 +254,18 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp, the same on every call.  Code that issues
+// tcgen05.mma goes behind this and not behind a lane number: the compiler then
+// knows that a single thread is left and feeds the instruction's uniform
+// operands directly.  Behind `lane == 0` a 128 x 128 x 16 MMA took 89 cycles to
+// issue, behind elect.sync 60, i.e. its execution time (measured on the
+// backward pass's dQ kernel without its element-wise work).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {

@@ -313,7 +313,7 @@ comp_pair_kernel(const __grid_constant__ CompMaps maps, const CompArgs a, const 
         __syncwarp();
     } else if (warp == 9) {
         // ================= MMA issuer =================
-        if (lane == 0 && any) {
+        if (any && elect_one()) {
             constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlock, false);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
             const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
