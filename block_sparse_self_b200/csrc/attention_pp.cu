@@ -169,8 +169,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // handling; a separate instantiation keeps that code out of the common case.
 // BIAS (window mode only): a relative position bias is added to the logits,
 // one value per tile where its offsets share a bucket, else by shuffles (see
-// relative_bias.cuh).  S then becomes scale*log2e*S + bias on its way
-// out of tensor memory and the softmax below runs with a scale of 1.
+// relative_bias.cuh).
 template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
@@ -426,7 +425,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         }
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t s_col = t * 128, o_col = C::O_COL + t * D;
-        const float sl2 = BIAS ? 1.f : a.scale_log2;
+        const float sl2 = a.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -459,22 +458,24 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                     }
                 }
             }
+            // with a bias: x is scaled and biased here where the tile needs a value
+            // per offset, else the scale and the tile's one value go into the
+            // exponents' fma (mul, add) like the scale alone does without one
+            [[maybe_unused]] float mul = a.scale_log2, add = 0.f;
+            [[maybe_unused]] bool flat = true;
+            [[maybe_unused]] const float *E = nullptr;
+            if constexpr (BIAS) {
+                E = a.bias_E + static_cast<size_t>(bh % a.n_heads) * (2 * a.bias_R + 1) + a.bias_R;
+                const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
+                int bucket;
+                flat = bias_uniform(a.bias_bm + a.bias_R, a.bias_R, d, bucket);
+                if (flat) add = __ldg(E + min(max(d, -a.bias_R), a.bias_R));
+                else mul = 1.f;
+            }
             auto apply_bias = [&]() {
                 if constexpr (BIAS) {
-                    const float *E = a.bias_E + static_cast<size_t>(bh % a.n_heads) * (2 * a.bias_R + 1) + a.bias_R;
-                    const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
-                    int bucket;
-                    if (bias_uniform(a.bias_bm + a.bias_R, a.bias_R, d, bucket)) {
-                        const float b = __ldg(E + min(max(d, -a.bias_R), a.bias_R));
-                        const uint64_t sx = f32x2(a.scale_log2, a.scale_log2), bx = f32x2(b, b);
-                        #pragma unroll
-                        for (int c = 0; c < BN; c += 2) {
-                            float y0, y1;
-                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sx, bx), y0, y1);
-                            x[c] = __float_as_uint(y0);
-                            x[c + 1] = __float_as_uint(y1);
-                        }
-                    } else {
+                    if (!flat) {
+                        const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
                         #pragma unroll
                         for (int u = 0; u < BN / 32; ++u) {
                             const BiasPiece piece = bias_piece(E, a.bias_R, 1, d + 32 * u - wq * 32, lane);
@@ -536,7 +537,8 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             // each half of the packed pair as it is; unpacking the pair first for
             // two-wide adds measured a few percent slower.
             auto exp_pass = [&](float m_use) -> float {
-                const uint64_t sl2x2 = f32x2(sl2, sl2), nmx2 = f32x2(-m_use, -m_use);
+                const float f = BIAS ? mul : sl2, c0 = BIAS ? add - m_use : -m_use;
+                const uint64_t sl2x2 = f32x2(f, f), nmx2 = f32x2(c0, c0);
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
                 #pragma unroll
                 for (int q = 0; q < BN / 2; ++q) {
@@ -561,7 +563,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             };
             // first visible keys of this row: take the block max before the exponentials
-            if (m_ref == -INFINITY) m_ref = raw_max() * sl2;  // may stay -inf
+            if (m_ref == -INFINITY) m_ref = BIAS ? fmaf(raw_max(), mul, add) : raw_max() * sl2;  // may stay -inf
             // The running max is lazy: every P is at most the row sum, so a sum
             // above kMaxRowSum (or inf) means the row's max grew; then O and l are
             // rescaled and the block is redone from S, still intact in TMEM.
@@ -577,7 +579,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 tmem_ld_wait();
                 apply_bias();
                 apply_mask();
-                const float m_new = need ? fmaxf(m_ref, raw_max() * sl2) : m_ref;
+                const float m_new = need ? fmaxf(m_ref, BIAS ? fmaf(raw_max(), mul, add) : raw_max() * sl2) : m_ref;
                 if (j > 0) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, abort_flag))) {
                         ok = false;

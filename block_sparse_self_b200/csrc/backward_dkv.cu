@@ -266,21 +266,40 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
         const float sl2 = a.scale_log2;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
+            if (BS < 128 && !rows_live) {  // rows past the block: keep the barriers' phases
+                if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag))) { ok = false; break; }
+                if (lane == 0) mbar_arrive(p_full);
+                if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
+                if (lane == 0) mbar_arrive(ds_full);
+                continue;
+            }
             const int qs = j % C::NQ;
-            // the statistics arrived with Q, before S was computed; waiting on
-            // their own barrier makes them visible to this thread
-            if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, abort_flag) &&
-                                             mbar_wait(&q_full[qs], (j / C::NQ) & 1, abort_flag))) {
+            // the statistics arrive with Q, before S is computed: -lse is in registers
+            // by the time S is
+            bool got = mbar_wait(&q_full[qs], (j / C::NQ) & 1, abort_flag);
+            float nlr[64];
+            {
+                const float4 *nl = reinterpret_cast<const float4 *>(sStat + qs * 256 + 64 * hf);
+                #pragma unroll
+                for (int c4 = 0; c4 < 16; ++c4) {
+                    const float4 l4 = nl[c4];
+                    nlr[4 * c4] = l4.x;
+                    nlr[4 * c4 + 1] = l4.y;
+                    nlr[4 * c4 + 2] = l4.z;
+                    nlr[4 * c4 + 3] = l4.w;
+                }
+            }
+            got = got && mbar_wait(s_full, j & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             float pr[64];
-            if (rows_live) {
+            {
                 uint32_t x[64];
                 tmem_ld32(t_lane + C::S_COL + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
                 tmem_ld32(t_lane + C::S_COL + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                const float4 *nl = reinterpret_cast<const float4 *>(sStat + qs * 256 + 64 * hf);
                 // which of the 64 columns this row's key is seen from
                 uint32_t see[2] = {~0u, ~0u};
                 bool masked = false;
@@ -321,23 +340,13 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                 // that the exponentials below are one straight run
                 const uint64_t sl2x2 = f32x2(sl2, sl2);
                 #pragma unroll
-                for (int c4 = 0; c4 < 16; ++c4) {
-                    const float4 l4 = nl[c4];
-                    float y0, y1, y2, y3;
-                    uint64_t b0 = f32x2(l4.x, l4.y), b1 = f32x2(l4.z, l4.w);
-                    if constexpr (BIAS) {
-                        b0 = add_f32x2(b0, f32x2(flat, flat));
-                        b1 = add_f32x2(b1, f32x2(flat, flat));
-                    }
-                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4]), __uint_as_float(x[4 * c4 + 1])), sl2x2, b0),
-                                y0, y1);
-                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[4 * c4 + 2]), __uint_as_float(x[4 * c4 + 3])), sl2x2,
-                                          b1),
-                                y2, y3);
-                    x[4 * c4] = __float_as_uint(y0);
-                    x[4 * c4 + 1] = __float_as_uint(y1);
-                    x[4 * c4 + 2] = __float_as_uint(y2);
-                    x[4 * c4 + 3] = __float_as_uint(y3);
+                for (int c = 0; c < 64; c += 2) {
+                    float y0, y1;
+                    uint64_t b = f32x2(nlr[c], nlr[c + 1]);
+                    if constexpr (BIAS) b = add_f32x2(b, f32x2(flat, flat));
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, b), y0, y1);
+                    x[c] = __float_as_uint(y0);
+                    x[c + 1] = __float_as_uint(y1);
                 }
                 if constexpr (BIAS) {
                     if (!uniform) {
@@ -366,7 +375,7 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
             if (lane == 0) mbar_arrive(p_full);
             if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
-            if (rows_live) {
+            {
                 const float4 *nd = reinterpret_cast<const float4 *>(sStat + qs * 256 + 128 + 64 * hf);
                 uint32_t dsk[32];
                 #pragma unroll

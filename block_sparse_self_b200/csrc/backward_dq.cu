@@ -298,10 +298,16 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
         };
         bool ok = true;
         for (int j = 0; j < n; ++j) {
+            if (BS < 128 && !rows_live) {  // rows past the block: keep the barriers' phases
+                if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag))) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
+                if (lane == 0) mbar_arrive(ds_full);
+                continue;
+            }
             // which of the 64 columns this row sees
             uint32_t see[2] = {~0u, ~0u};
             bool masked = false;
-            if (rows_live) {
+            {
                 if constexpr (WINDOW) {
                     const int q0 = qb * 128, ks = w.at(j) * 128;
                     masked = !((ks + 128 <= a.P) && (a.dense || ks + 128 <= a.sink ||
@@ -333,7 +339,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
             float pr[64];
             [[maybe_unused]] bool uniform = true;
             [[maybe_unused]] int bucket = 0, diag0 = 0;
-            if (rows_live) {
+            {
                 uint32_t x[64];
                 tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
                 tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
@@ -381,7 +387,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
             }
             if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
-            if (rows_live) {
+            {
                 uint32_t dsk[32];
                 const uint64_t ndx2 = f32x2(nd, nd);
                 #pragma unroll
