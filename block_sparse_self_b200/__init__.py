@@ -73,17 +73,17 @@ def lib() -> ctypes.CDLL:
         "vsa_centroid_compensated_attention": ([P, P, P, P, I, I, I, I, I, I, P, P, I, I, F, P, SZ, P], I),
         "vsa_centroid_compensated_attention_tiled": ([P, P, P, P, I, I, I, I, I, D3, P, I, P, P, P, I, I, F, P, SZ, P],
                                                      I),
-        "vsa_block_sparse_attention_lse": ([P, P, P, P, I, P, I, I, I, I, I, P, P, I, I, I, F, P], I),
-        "vsa_block_sparse_attention_tiled_lse": ([P, P, P, P, I, P, I, I, I, I, D3, P, I, P, P, P, I, I, I, F, P], I),
+        "vsa_block_sparse_attention_lse": ([P, P, P, P, I, P, P, I, I, I, I, I, P, P, I, I, I, F, P], I),
+        "vsa_block_sparse_attention_tiled_lse": ([P, P, P, P, I, P, P, I, I, I, I, D3, P, I, P, P, P, I, I, I, F, P], I),
         "vsa_window_attention_lse_workspace_size": ([I, I, I, I], SZ),
-        "vsa_window_attention_lse": ([P, P, P, P, I, P, I, I, I, I, I, I, F, P, I, I, I, P, SZ, P], I),
+        "vsa_window_attention_lse": ([P, P, P, P, I, P, P, I, I, I, I, I, I, F, P, I, I, I, P, SZ, P], I),
         "vsa_block_sparse_attention_backward_workspace_size": ([I, I, I, I, I, I], SZ),
-        "vsa_block_sparse_attention_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, P, P, I, I, I, F, P,
+        "vsa_block_sparse_attention_backward": ([P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, I, P, P, I, I, I, F, P,
                                                  SZ, P], I),
-        "vsa_block_sparse_attention_tiled_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, D3, P, I, P, P, P,
+        "vsa_block_sparse_attention_tiled_backward": ([P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, D3, P, I, P, P, P,
                                                        I, I, I, F, P, SZ, P], I),
         "vsa_window_attention_backward_workspace_size": ([I, I, I, I, I], SZ),
-        "vsa_window_attention_backward": ([P, P, P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, F, P, I, I, I, P, P, SZ,
+        "vsa_window_attention_backward": ([P, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, I, I, F, P, I, I, I, P, P, SZ,
                                            P], I),
         "vsa_relative_position_buckets": ([I, I, P, P], I),
         "vsa_transpose_block_lists_workspace_size": ([I, I], SZ),
@@ -506,7 +506,7 @@ def _scale(scale) -> float:
     return 0.0 if scale is None else float(scale)
 
 
-def _check_saved(do, q, o, lse):
+def _check_saved(do, q, o, lse, o_lo):
     """The forward pass's output and the gradient that comes back for it."""
     B, H, S, D = q.shape
     if tuple(do.shape) != (B, H, S, D) or tuple(o.shape) != (B, H, S, D):
@@ -516,6 +516,22 @@ def _check_saved(do, q, o, lse):
     _cuda(lse, "lse")
     if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, S):
         raise ValueError(f"lse must be float32 of shape {(B, H, S)}, as the forward call returns it")
+    if o_lo is not None:
+        _cuda(o_lo, "o_lo")
+        if o_lo.dtype != torch.bfloat16 or o.dtype != torch.bfloat16 or o_lo.shape != o.shape:
+            raise ValueError("o_lo must be the bfloat16 remainder that the forward call returned beside a bfloat16 o")
+
+
+def _saved_outputs(o, remainder: bool):
+    """lse and, beside a bf16 o, its remainder if asked for: what a forward call writes for the backward pass."""
+    lse = torch.empty(o.shape[:-1], dtype=torch.float32, device=o.device)
+    return lse, torch.empty_like(o) if remainder and o.dtype == torch.bfloat16 else None
+
+
+def _saved(o, lse, o_lo, return_lse, return_remainder):
+    if return_remainder:
+        return o, lse, o_lo
+    return (o, lse) if return_lse else o
 
 
 class _BlockSparse(torch.autograd.Function):
@@ -524,41 +540,44 @@ class _BlockSparse(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, fwd, bwd, args, kw, out_dtype):
         qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-        o, lse = fwd(qb, kb, vb, *args, out_dtype=_out_dtype(out_dtype, q), return_lse=True, **kw)
+        o, lse, o_lo = fwd(qb, kb, vb, *args, out_dtype=_out_dtype(out_dtype, q), return_remainder=True, **kw)
         tensors = [a for a in args if isinstance(a, torch.Tensor)]
         ctx.where = [isinstance(a, torch.Tensor) for a in args]
         ctx.rest = [a for a in args if not isinstance(a, torch.Tensor)]
         ctx.bwd, ctx.kw, ctx.dtypes = bwd, kw, (q.dtype, k.dtype, v.dtype)
-        ctx.save_for_backward(qb, kb, vb, o, lse, *tensors)
-        ctx.mark_non_differentiable(lse)
+        ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, *tensors)
+        ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
-        return o, lse
+        return o, lse, o_lo
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, do, _):
+    def backward(ctx, do, *_):
         if do is None:
             return (None,) * 8
-        qb, kb, vb, o, lse, *tensors = ctx.saved_tensors
+        qb, kb, vb, o, lse, o_lo, *tensors = ctx.saved_tensors
         tensors, rest = iter(tensors), iter(ctx.rest)
         args = [next(tensors) if t else next(rest) for t in ctx.where]
         f32 = any(t == torch.float32 for t in ctx.dtypes)
-        grads = ctx.bwd(do.contiguous(), qb, kb, vb, o, lse, *args, grad_dtype=torch.float32 if f32 else torch.bfloat16,
-                        **ctx.kw)
+        grads = ctx.bwd(do.contiguous(), qb, kb, vb, o, lse, *args, o_lo=o_lo,
+                        grad_dtype=torch.float32 if f32 else torch.bfloat16, **ctx.kw)
         return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (None,) * 5
 
 
 def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, scale: Optional[float] = None,
-                           out_dtype=None, return_lse: bool = False):
+                           out_dtype=None, return_lse: bool = False, return_remainder: bool = False):
     """Softmax attention of each query block over the key blocks its list names (tile-contiguous order).
 
     return_lse=True also returns the natural log of each row's softmax sum
-    (fp32 [B, H, S]), which block_sparse_attention_backward takes.
+    (fp32 [B, H, S]), which block_sparse_attention_backward takes, and
+    return_remainder=True what rounding the output to bf16 left as well
+    (o, lse, o_lo; None for an fp32 output): with it the backward pass is as
+    exact as with an fp32 output.
     Differentiable in q, k and v; the lists are constants of the backward pass."""
     if _wants_grad(q, k, v):
-        o, lse = _BlockSparse.apply(q, k, v, block_sparse_attention, block_sparse_attention_backward,
-                                    (idx, cnt, block), dict(group_size=group_size, scale=scale), out_dtype)
-        return (o, lse) if return_lse else o
+        o, lse, o_lo = _BlockSparse.apply(q, k, v, block_sparse_attention, block_sparse_attention_backward,
+                                          (idx, cnt, block), dict(group_size=group_size, scale=scale), out_dtype)
+        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
@@ -566,13 +585,13 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     per_head = idx.dim() == 4
     cap = idx.shape[-1]
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    if return_lse:
-        lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device)
-        _check(lib().vsa_block_sparse_attention_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), B, H,
-                                                    S, D, int(block), _ptr(idx), _ptr(cnt), int(cap),
+    if return_lse or return_remainder:
+        lse, o_lo = _saved_outputs(o, return_remainder)
+        _check(lib().vsa_block_sparse_attention_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse),
+                                                    _ptr(o_lo), B, H, S, D, int(block), _ptr(idx), _ptr(cnt), int(cap),
                                                     1 if per_head else 0, int(group_size), _scale(scale),
                                                     _stream(q.device)))
-        return o, lse
+        return _saved(o, lse, o_lo, return_lse, return_remainder)
     _check(lib().vsa_block_sparse_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(block),
                                             _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size),
                                             _scale(scale), _stream(q.device)))
@@ -580,24 +599,25 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
 
 
 def block_sparse_attention_backward(do, q, k, v, o, lse, idx, cnt, block: int, group_size: int = 0,
-                                    scale: Optional[float] = None, grad_dtype=None):
+                                    scale: Optional[float] = None, grad_dtype=None,
+                                    o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention for the gradient `do` of its output, from that output
-    and its lse.  The gradients have q's type unless grad_dtype says otherwise."""
+    and its lse (and its remainder o_lo, if the forward call returned one).  The gradients have q's type unless grad_dtype says otherwise."""
     B, H, S, D = _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
-    _check_saved(do, q, o, lse)
+    _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
     if block not in (32, 64, 128) or S % block:
         raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
     _check_lists(idx, cnt, B, H, S // block)
-    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, idx=idx, cnt=cnt)
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt)
     cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
     with torch.cuda.device(q.device):
         need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, S, int(block), cap, per_head)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         _check(lib().vsa_block_sparse_attention_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
             _code(gdt), B, H, S, D, int(block), _ptr(idx), _ptr(cnt), cap, per_head, int(group_size), _scale(scale),
             _ptr(ws), need, _stream(q.device)))
     return dq, dk, dv
@@ -682,18 +702,19 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
 
 
 def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: Optional[float] = None,
-                                 out_dtype=None, group_stride: int = 0, return_lse: bool = False):
+                                 out_dtype=None, group_stride: int = 0, return_lse: bool = False,
+                                 return_remainder: bool = False):
     """unpermute(block_sparse_attention(permute(q), permute(k), permute(v), idx, cnt, block)) in one
     kernel: q, k, v and the result stay in T-major order; lists number the blocks of each
     head's tile-contiguous order (block = the tile volume if 32 or 64, else 128 tokens).
     group_stride s > 0 (128-token blocks) restricts each query to keys whose position
-    differs from its own by a multiple of s (see include/vsa.h).  return_lse and
-    differentiability as for block_sparse_attention; lse is in T-major order."""
+    differs from its own by a multiple of s (see include/vsa.h).  return_lse,
+    return_remainder and differentiability as for block_sparse_attention; all in T-major order."""
     if _wants_grad(q, k, v):
-        o, lse = _BlockSparse.apply(q, k, v, block_sparse_attention_tiled, block_sparse_attention_tiled_backward,
-                                    (grid, tiles, choice, idx, cnt), dict(scale=scale, group_stride=group_stride),
-                                    out_dtype)
-        return (o, lse) if return_lse else o
+        o, lse, o_lo = _BlockSparse.apply(q, k, v, block_sparse_attention_tiled, block_sparse_attention_tiled_backward,
+                                          (grid, tiles, choice, idx, cnt),
+                                          dict(scale=scale, group_stride=group_stride), out_dtype)
+        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
@@ -702,22 +723,23 @@ def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: 
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     tail = (B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), int(idx.shape[-1]),
             1 if idx.dim() == 4 else 0, int(group_stride), _scale(scale), _stream(q.device))
-    if return_lse:
-        lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device)
+    if return_lse or return_remainder:
+        lse, o_lo = _saved_outputs(o, return_remainder)
         _check(lib().vsa_block_sparse_attention_tiled_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse),
-                                                          *tail))
-        return o, lse
+                                                          _ptr(o_lo), *tail))
+        return _saved(o, lse, o_lo, return_lse, return_remainder)
     _check(lib().vsa_block_sparse_attention_tiled(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), *tail))
     return o
 
 
 def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choice, idx, cnt,
-                                          scale: Optional[float] = None, group_stride: int = 0, grad_dtype=None):
+                                          scale: Optional[float] = None, group_stride: int = 0, grad_dtype=None,
+                                          o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention_tiled, all in T-major order, for the gradient `do` of its
-    output, from that output and its lse.  The gradients have q's type unless grad_dtype says otherwise."""
+    output, from that output and its lse (and its remainder o_lo, if there is one).  The gradients have q's type unless grad_dtype says otherwise."""
     B, H, S, D = _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
-    _check_saved(do, q, o, lse)
+    _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
     arr, n = _tiles_arg(tiles)
     positions = _grid_tokens(padded_grid(grid, tiles))
@@ -725,14 +747,14 @@ def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choi
     if block not in (32, 64, 128) or positions % block:
         raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {math.prod(tiles[0])}")
     _check_lists(idx, cnt, B, H, positions // block)
-    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, idx=idx, cnt=cnt, choice=choice)
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt, choice=choice)
     cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
     with torch.cuda.device(q.device):
         need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, positions, block, cap, per_head)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         _check(lib().vsa_block_sparse_attention_tiled_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
             _code(gdt), B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), cap,
             per_head, int(group_stride), _scale(scale), _ptr(ws), need, _stream(q.device)))
     return dq, dk, dv
@@ -765,56 +787,55 @@ class _Window(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, bias, window, kw, out_dtype):
         qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-        o, lse = window_attention(qb, kb, vb, window, out_dtype=_out_dtype(out_dtype, q), bias=bias, return_lse=True,
-                                  **kw)
+        o, lse, o_lo = window_attention(qb, kb, vb, window, out_dtype=_out_dtype(out_dtype, q), bias=bias,
+                                        return_remainder=True, **kw)
         ctx.window, ctx.kw, ctx.dtypes = window, kw, (q.dtype, k.dtype, v.dtype)
-        ctx.save_for_backward(qb, kb, vb, o, lse, bias)
-        ctx.mark_non_differentiable(lse)
+        ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, bias)
+        ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
-        return o, lse
+        return o, lse, o_lo
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, do, _):
+    def backward(ctx, do, *_):
         if do is None:
             return (None,) * 7
-        qb, kb, vb, o, lse, bias = ctx.saved_tensors
+        qb, kb, vb, o, lse, o_lo, bias = ctx.saved_tensors
         f32 = any(t == torch.float32 for t in ctx.dtypes)
         kw = {n: x for n, x in ctx.kw.items() if n != "chunk_size"}
         grads = window_attention_backward(do.contiguous(), qb, kb, vb, o, lse, ctx.window, bias=bias,
                                           grad_dtype=torch.float32 if f32 else torch.bfloat16,
-                                          bias_grad=ctx.needs_input_grad[3], **kw)
+                                          bias_grad=ctx.needs_input_grad[3], o_lo=o_lo, **kw)
         dbias = grads[3] if ctx.needs_input_grad[3] else None
         return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (dbias, None, None, None)
 
 
 def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float] = None,
                      chunk_size: Optional[int] = None, out_dtype=None, bias: Optional[torch.Tensor] = None,
-                     max_distance: int = 128, return_lse: bool = False):
+                     max_distance: int = 128, return_lse: bool = False, return_remainder: bool = False):
     """Symmetric sliding-window attention with `sink` global keys (dense when window >= S).
 
     bias ([num_buckets, H], float32 or bfloat16) is a learned relative position
     bias: bias[bucket(j - i), h] is added to the scaled logit of query i and key
     j of head h, with the buckets of relative_position_buckets(num_buckets,
-    max_distance).  return_lse=True also returns the natural log of each row's
-    softmax sum (fp32 [B, H, S]), which window_attention_backward takes.
+    max_distance).  return_lse and return_remainder as for block_sparse_attention.
     Differentiable in q, k, v and bias."""
     if _wants_grad(q, k, v, bias):
         kw = dict(sink=sink, scale=scale, chunk_size=chunk_size, max_distance=max_distance)
-        o, lse = _Window.apply(q, k, v, bias, window, kw, out_dtype)
-        return (o, lse) if return_lse else o
+        o, lse, o_lo = _Window.apply(q, k, v, bias, window, kw, out_dtype)
+        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     if chunk_size is not None and int(chunk_size) < 1:
         raise ValueError(f"chunk_size must be >= 1, got {chunk_size}")
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    if bias is None and not return_lse:
+    if bias is None and not (return_lse or return_remainder):
         _check(lib().vsa_window_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(window),
                                           int(sink), _scale(scale), 0 if chunk_size is None else int(chunk_size),
                                           _stream(q.device)))
         return o
-    lse = torch.empty(B, H, S, dtype=torch.float32, device=q.device) if return_lse else None
+    lse, o_lo = _saved_outputs(o, return_remainder) if return_lse or return_remainder else (None, None)
     buckets, need, ws = 0, 0, None
     _same_device(q, k=k, v=v, bias=bias)
     with torch.cuda.device(q.device):
@@ -823,23 +844,23 @@ def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float]
             need = lib().vsa_window_attention_lse_workspace_size(H, S, buckets, int(max_distance))
             ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         _check(lib().vsa_window_attention_lse(
-            _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), B, H, S, D, int(window), int(sink),
+            _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), _ptr(o_lo), B, H, S, D, int(window), int(sink),
             _scale(scale), _ptr(bias), F32 if bias is None else _code(bias.dtype), buckets, int(max_distance),
             _ptr(ws), need, _stream(q.device)))
-    return (o, lse) if return_lse else o
+    return _saved(o, lse, o_lo, return_lse, return_remainder)
 
 
 def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, scale: Optional[float] = None,
                               bias: Optional[torch.Tensor] = None, max_distance: int = 128, grad_dtype=None,
-                              bias_grad: bool = True):
+                              bias_grad: bool = True, o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of window_attention for the gradient `do` of its output, from that output and its
-    lse; with a bias (dq, dk, dv, dbias), dbias in the bias's type, or None with bias_grad=False.
+    lse (and its remainder o_lo, if there is one); with a bias (dq, dk, dv, dbias), dbias in the bias's type, or None with bias_grad=False.
     The gradients of q, k and v have q's type unless grad_dtype says otherwise."""
     B, H, S, D = _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
-    _check_saved(do, q, o, lse)
+    _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
-    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, bias=bias)
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, bias=bias)
     buckets = 0 if bias is None else _bias_arg(bias, H)
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
     dbias = None if bias is None or not bias_grad else torch.empty_like(bias)
@@ -847,7 +868,7 @@ def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, s
         need = lib().vsa_window_attention_backward_workspace_size(B, H, S, buckets, int(max_distance))
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         _check(lib().vsa_window_attention_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
             _code(gdt), B, H, S, D, int(window), int(sink), _scale(scale), _ptr(bias),
             F32 if bias is None else _code(bias.dtype), buckets, int(max_distance), _ptr(dbias), _ptr(ws), need,
             _stream(q.device)))

@@ -731,6 +731,19 @@ vsa_status vsa_window_attention(const void *q, const void *k, const void *v, voi
 
 // ---- training: forward passes that keep the log-sum-exp, and backward passes ----
 
+// o_lo: [B, n_heads, S, D] bf16 beside a bf16 o, or NULL
+static vsa_status check_remainder(const void *o_lo, const void *o, vsa_dtype out_dtype, const float *lse, const void *q,
+                                  const void *k, const void *v, int BH, int S, int D) {
+    if (!o_lo) return VSA_OK;
+    VSA_REQUIRE(aligned16(o_lo), "o_lo must be NULL or a 16-byte aligned device pointer");
+    VSA_REQUIRE(out_dtype == VSA_BF16, "o_lo is what rounding o to bf16 leaves: out_dtype must be VSA_BF16");
+    const size_t n = static_cast<size_t>(BH) * S * D * 2;
+    VSA_REQUIRE(!overlaps(o_lo, n, o, n) && !overlaps(o_lo, n, q, n) && !overlaps(o_lo, n, k, n) &&
+                    !overlaps(o_lo, n, v, n) && !(lse && overlaps(o_lo, n, lse, static_cast<size_t>(BH) * S * 4)),
+                "o_lo must not overlap q, k, v, o or lse");
+    return VSA_OK;
+}
+
 static vsa_status check_lse(const float *lse, const void *o, size_t o_bytes, const void *q, const void *k, const void *v,
                             int BH, int S, int D) {
     VSA_REQUIRE(aligned4(lse), "lse must be a non-NULL 4-byte aligned device pointer");
@@ -759,21 +772,23 @@ static vsa_status check_bias(const void *bias, vsa_dtype bias_dtype, int num_buc
 }
 
 vsa_status vsa_block_sparse_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
-                                          float *lse, int B, int n_heads, int S, int D, int block, const int32_t *idx,
+                                          float *lse, void *o_lo, int B, int n_heads, int S, int D, int block, const int32_t *idx,
                                           const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
                                           void *stream) {
     VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
     AttnLaunch L;
     VSA_TRY(lists_launch(q, k, v, B, n_heads, S, D, block, idx, cnt, cap, list_per_head, group_size, scale, &L));
     VSA_TRY(check_lse(lse, o, static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype), q, k, v, L.BH, S, D));
+    VSA_TRY(check_remainder(o_lo, o, out_dtype, lse, q, k, v, L.BH, S, D));
     L.o = o;
     L.out_f32 = out_dtype == VSA_F32;
     L.lse = lse;
+    L.o_lo = o_lo;
     return launch_attention(L, status_or_null(stream), as_stream(stream));
 }
 
 vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, const void *v, void *o,
-                                                vsa_dtype out_dtype, float *lse, int B, int n_heads, int S, int D,
+                                                vsa_dtype out_dtype, float *lse, void *o_lo, int B, int n_heads, int S, int D,
                                                 vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
                                                 const int32_t *choice, const int32_t *idx, const int32_t *cnt, int cap,
                                                 int list_per_head, int group_stride, float scale, void *stream) {
@@ -782,9 +797,11 @@ vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, co
     VSA_TRY(tiled_launch(q, k, v, B, n_heads, S, D, grid, tiles, n_tiles, choice, idx, cnt, cap, list_per_head,
                          group_stride, scale, &L));
     VSA_TRY(check_lse(lse, o, static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype), q, k, v, L.BH, S, D));
+    VSA_TRY(check_remainder(o_lo, o, out_dtype, lse, q, k, v, L.BH, S, D));
     L.o = o;
     L.out_f32 = out_dtype == VSA_F32;
     L.lse = lse;
+    L.o_lo = o_lo;
     return launch_attention(L, status_or_null(stream), as_stream(stream));
 }
 
@@ -792,11 +809,11 @@ size_t vsa_window_attention_lse_workspace_size(int n_heads, int S, int num_bucke
     if (n_heads < 1 || S < 1 || num_buckets == 0) return 0;
     if (num_buckets < 4 || num_buckets > 256 || num_buckets % 2 != 0) return 0;
     if (max_distance <= num_buckets / 4 || max_distance > (1 << 24)) return 0;
-    return bias_workspace_bytes(n_heads, S, max_distance);
+    return bias_workspace_bytes(n_heads, S, num_buckets, max_distance);
 }
 
 vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
-                                    float *lse, int B, int n_heads, int S, int D, int window, int sink, float scale,
+                                    float *lse, void *o_lo, int B, int n_heads, int S, int D, int window, int sink, float scale,
                                     const void *bias, vsa_dtype bias_dtype, int num_buckets, int max_distance,
                                     void *workspace, size_t workspace_bytes, void *stream) {
     VSA_TRY(check_attention_common(q, k, v, o, out_dtype, B, n_heads, S, D, scale));
@@ -804,9 +821,11 @@ vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v,
     VSA_TRY(window_launch(q, k, v, B, n_heads, S, D, window, sink, scale, &L));
     const size_t o_bytes = static_cast<size_t>(L.BH) * S * D * esize_of(out_dtype);
     if (lse) VSA_TRY(check_lse(lse, o, o_bytes, q, k, v, L.BH, S, D));
+    VSA_TRY(check_remainder(o_lo, o, out_dtype, lse, q, k, v, L.BH, S, D));
     L.o = o;
     L.out_f32 = out_dtype == VSA_F32;
     L.lse = lse;
+    L.o_lo = o_lo;
     if (bias) {
         VSA_TRY(check_bias(bias, bias_dtype, num_buckets, max_distance));
         const size_t need = vsa_window_attention_lse_workspace_size(n_heads, S, num_buckets, max_distance);
@@ -815,13 +834,15 @@ vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v,
         VSA_REQUIRE(!overlaps(workspace, need, o, o_bytes) && !overlaps(workspace, need, q, in) &&
                         !overlaps(workspace, need, k, in) && !overlaps(workspace, need, v, in) &&
                         !(lse && overlaps(workspace, need, lse, static_cast<size_t>(L.BH) * S * 4)) &&
+                        !(o_lo && overlaps(workspace, need, o_lo, in)) &&
                         !overlaps(workspace, need, bias,
                                   static_cast<size_t>(num_buckets) * n_heads * esize_of(bias_dtype)),
-                    "workspace must not overlap q, k, v, o, lse or bias");
+                    "workspace must not overlap q, k, v, o, lse, o_lo or bias");
         L.n_heads = n_heads;
+        L.buckets = num_buckets;
         L.bias_R = bias_reach(S, max_distance);
         VSA_TRY(check_cuda(launch_bias_expand(bias, bias_dtype == VSA_F32, n_heads, S, num_buckets, max_distance,
-                                              workspace, &L.bias_E, &L.bias_bm, as_stream(stream)),
+                                              workspace, &L.bias_tab, &L.bias_bm, as_stream(stream)),
                            "relative bias launch"));
     }
     return launch_attention(L, status_or_null(stream), as_stream(stream));
@@ -863,7 +884,7 @@ vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int
 }
 
 // Checks of a backward pass beyond the launch's own, then the launch.
-static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq, void *dk,
                            void *dv, vsa_dtype grad_dtype, int B, int n_heads, const AttnLaunch &L, const void *bias,
                            vsa_dtype bias_dtype, int num_buckets, int max_distance, void *dbias, void *workspace,
                            size_t workspace_bytes, void *stream) {
@@ -875,6 +896,8 @@ static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, cons
         VSA_REQUIRE(static_cast<long long>(L.nb) * L.cap <= 0x7fffffffLL, "nb * cap must be < 2^31");
     VSA_REQUIRE(static_cast<long long>(BH) * ((L.tiled ? L.nb : (L.S + L.block - 1) / L.block)) <= 0x7fffffffLL,
                 "too many blocks for one launch");
+    VSA_REQUIRE(o_lo == nullptr || (aligned16(o_lo) && o_dtype == VSA_BF16),
+                "o_lo must be NULL, or 16-byte aligned beside a bf16 o");
     if (bias) VSA_TRY(check_bias(bias, bias_dtype, num_buckets, max_distance));
     VSA_REQUIRE(bias != nullptr || dbias == nullptr, "dbias needs a bias");
     VSA_REQUIRE(dbias == nullptr || aligned4(dbias), "dbias must be NULL or 4-byte aligned");
@@ -890,15 +913,17 @@ static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, cons
         {dq, n * esize_of(grad_dtype)}, {dk, n * esize_of(grad_dtype)}, {dv, n * esize_of(grad_dtype)},
         {workspace, need}, {dbias, dbias ? table : 0},
         {L.q, n * 2}, {L.k, n * 2}, {L.v, n * 2}, {g, n * 2}, {o, n * esize_of(o_dtype)},
-        {lse, static_cast<size_t>(BH) * L.S * 4}, {bias, table}, {L.idx, lists * L.cap * 4}, {L.cnt, lists * 4}};
+        {lse, static_cast<size_t>(BH) * L.S * 4}, {bias, table}, {L.idx, lists * L.cap * 4}, {L.cnt, lists * 4},
+        {o_lo, o_lo ? n * 2 : 0}};
     for (int x = 0; x < 5; ++x)
-        for (int y = x + 1; y < 14; ++y)
+        for (int y = x + 1; y < 15; ++y)
             VSA_REQUIRE(buf[x].n == 0 || buf[y].n == 0 || !overlaps(buf[x].p, buf[x].n, buf[y].p, buf[y].n),
                         "dq, dk, dv, dbias and workspace must not overlap one another or an input");
     BackwardLaunch W{};
     W.a = L;
     W.g = g;
     W.o = o;
+    W.o_lo = o_lo;
     W.o_f32 = o_dtype == VSA_F32;
     W.lse = lse;
     W.dq = dq;
@@ -936,7 +961,7 @@ size_t vsa_block_sparse_attention_backward_workspace_size(int B, int n_heads, in
 }
 
 vsa_status vsa_block_sparse_attention_backward(const void *dout, const void *q, const void *k, const void *v,
-                                               const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+                                               const void *o, vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq, void *dk,
                                                void *dv, vsa_dtype grad_dtype, int B, int n_heads, int S, int D,
                                                int block, const int32_t *idx, const int32_t *cnt, int cap,
                                                int list_per_head, int group_size, float scale, void *workspace,
@@ -944,12 +969,12 @@ vsa_status vsa_block_sparse_attention_backward(const void *dout, const void *q, 
     VSA_TRY(check_gradients(q, k, v, dq, dk, dv, grad_dtype, B, n_heads, S, D, scale));
     AttnLaunch L;
     VSA_TRY(lists_launch(q, k, v, B, n_heads, S, D, block, idx, cnt, cap, list_per_head, group_size, scale, &L));
-    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
+    return backward(dout, o, o_dtype, o_lo, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
                     workspace, workspace_bytes, stream);
 }
 
 vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const void *q, const void *k, const void *v,
-                                                     const void *o, vsa_dtype o_dtype, const float *lse, void *dq,
+                                                     const void *o, vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq,
                                                      void *dk, void *dv, vsa_dtype grad_dtype, int B, int n_heads,
                                                      int S, int D, vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
                                                      const int32_t *choice, const int32_t *idx, const int32_t *cnt,
@@ -959,7 +984,7 @@ vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const voi
     AttnLaunch L;
     VSA_TRY(tiled_launch(q, k, v, B, n_heads, S, D, grid, tiles, n_tiles, choice, idx, cnt, cap, list_per_head,
                          group_stride, scale, &L));
-    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
+    return backward(dout, o, o_dtype, o_lo, lse, dq, dk, dv, grad_dtype, B, n_heads, L, nullptr, VSA_F32, 0, 0, nullptr,
                     workspace, workspace_bytes, stream);
 }
 
@@ -970,7 +995,7 @@ size_t vsa_window_attention_backward_workspace_size(int B, int n_heads, int S, i
 }
 
 vsa_status vsa_window_attention_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
-                                         vsa_dtype o_dtype, const float *lse, void *dq, void *dk, void *dv,
+                                         vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq, void *dk, void *dv,
                                          vsa_dtype grad_dtype, int B, int n_heads, int S, int D, int window, int sink,
                                          float scale, const void *bias, vsa_dtype bias_dtype, int num_buckets,
                                          int max_distance, void *dbias, void *workspace, size_t workspace_bytes,
@@ -978,7 +1003,7 @@ vsa_status vsa_window_attention_backward(const void *dout, const void *q, const 
     VSA_TRY(check_gradients(q, k, v, dq, dk, dv, grad_dtype, B, n_heads, S, D, scale));
     AttnLaunch L;
     VSA_TRY(window_launch(q, k, v, B, n_heads, S, D, window, sink, scale, &L));
-    return backward(dout, o, o_dtype, lse, dq, dk, dv, grad_dtype, B, n_heads, L, bias, bias_dtype, num_buckets,
+    return backward(dout, o, o_dtype, o_lo, lse, dq, dk, dv, grad_dtype, B, n_heads, L, bias, bias_dtype, num_buckets,
                     max_distance, dbias, workspace, workspace_bytes, stream);
 }
 

@@ -47,6 +47,7 @@ struct AttnArgs {
     void *out;
     int out_f32;
     float *lse;  // optional per-row log-sum-exp, see AttnLaunch
+    void *o_lo;  // optional remainder of a bf16 o, see AttnLaunch
     int *status;
     // tiled mode
     int H, W;  // the padded grid's frame
@@ -506,6 +507,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
                                                 pack_bf16x2(__uint_as_float(u[4]) * inv, __uint_as_float(u[5]) * inv),
                                                 pack_bf16x2(__uint_as_float(u[6]) * inv, __uint_as_float(u[7]) * inv));
                         }
+                        if (a.o_lo) store_remainder(o, inv, static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D + 32 * c);
                     }
                 }
             }
@@ -521,6 +523,10 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
             } else {
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D);
                 for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.o_lo) {
+                    uint4 *lo = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D);
+                    for (int e = 0; e < D / 8; ++e) lo[e] = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
         }
     }
@@ -574,6 +580,7 @@ vsa_status run(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.out = L.o;
     a.out_f32 = L.out_f32;
     a.lse = L.lse;
+    a.o_lo = L.o_lo;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;

@@ -56,9 +56,10 @@ struct PPArgs {
     int out_f32;
     float2 *stats;  // optional per-row (m, l), see AttnLaunch
     float *lse;     // optional per-row log-sum-exp, see AttnLaunch
-    const float *bias_E;  // window mode with a relative position bias: log2e bias by offset,
+    void *o_lo;     // optional remainder of a bf16 o, see AttnLaunch
+    const float *bias_tab;   // window mode with a relative position bias: log2e bias by head and bucket,
     const uint8_t *bias_bm;  // and bucket by offset (see relative_bias.cu)
-    int bias_R, n_heads;
+    int bias_R, buckets, n_heads;
     int *status;
     // tiled mode: T-major tensors, per-head tiling (all of volume 128 * m)
     int H, W;         // the padded grid's frame (equal to the real one when nothing is padded)
@@ -192,10 +193,12 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *list_ok = reinterpret_cast<int *>(tmem_slot + 2);  // [2]
+    float *sTab = reinterpret_cast<float *>(tmem_slot + 4);  // BIAS: [kMaxBuckets]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.y;
     const int S = a.S;
+    if constexpr (BIAS) bias_table(sTab, a.bias_tab, bh % a.n_heads, a.buckets, threadIdx.x, kThreads);
     TileSched ts[2] = {make_sched<WINDOW>(a, 2 * blockIdx.x, bh), make_sched<WINDOW>(a, 2 * blockIdx.x + 1, bh)};
 
     if (threadIdx.x == 0) {
@@ -427,6 +430,16 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         const uint32_t s_col = t * 128, o_col = C::O_COL + t * D;
         const float sl2 = a.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
+        // buckets of a key tile's five runs of 32 offsets (this lane's of each)
+        [[maybe_unused]] int bk[5] = {0, 0, 0, 0, 0};
+        [[maybe_unused]] auto fetch_buckets = [&](int j) {
+            const int o0 = kblock_of<WINDOW>(sc, j) * BN - q0 - wq * 32 - 32 + lane;
+            #pragma unroll
+            for (int u = 0; u < 5; ++u) bk[u] = bias_bucket(a.bias_bm, a.bias_R, o0 + 32 * u);
+        };
+        if constexpr (BIAS) {
+            if (n > 0) fetch_buckets(0);
+        }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag))) { ok = false; break; }
@@ -458,31 +471,42 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                     }
                 }
             }
-            // with a bias: x is scaled and biased here where the tile needs a value
-            // per offset, else the scale and the tile's one value go into the
-            // exponents' fma (mul, add) like the scale alone does without one
+            // with a bias: x is scaled and biased here where the tile needs more than
+            // one value, else the scale and the one value go into the exponents'
+            // fma (mul, add) like the scale alone does without one
             [[maybe_unused]] float mul = a.scale_log2, add = 0.f;
             [[maybe_unused]] bool flat = true;
-            [[maybe_unused]] const float *E = nullptr;
             if constexpr (BIAS) {
-                E = a.bias_E + static_cast<size_t>(bh % a.n_heads) * (2 * a.bias_R + 1) + a.bias_R;
-                const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
-                int bucket;
-                flat = bias_uniform(a.bias_bm + a.bias_R, a.bias_R, d, bucket);
-                if (flat) add = __ldg(E + min(max(d, -a.bias_R), a.bias_R));
+                const int b0 = __shfl_sync(0xffffffffu, bk[4], 0);
+                flat = __all_sync(0xffffffffu, bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
+                if (flat) add = sTab[b0];
                 else mul = 1.f;
             }
             auto apply_bias = [&]() {
                 if constexpr (BIAS) {
                     if (!flat) {
-                        const int d = kblock_of<WINDOW>(sc, j) * BN - q0;
                         #pragma unroll
                         for (int u = 0; u < BN / 32; ++u) {
-                            const BiasPiece piece = bias_piece(E, a.bias_R, 1, d + 32 * u - wq * 32, lane);
-                            #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[32 * u + i] = __float_as_uint(fmaf(__uint_as_float(x[32 * u + i]), a.scale_log2,
-                                                                     bias_at(piece, i, lane)));
+                            // a bucket border crosses a few of the tile's 32 x 32 pieces only
+                            const BiasPiece piece = bias_piece(bk[u], bk[u + 1]);
+                            const float hi = sTab[piece.hi];
+                            if (piece.uniform) {
+                                const uint64_t sx = f32x2(a.scale_log2, a.scale_log2), bx = f32x2(hi, hi);
+                                #pragma unroll
+                                for (int i = 32 * u; i < 32 * u + 32; i += 2) {
+                                    float y0, y1;
+                                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sx, bx),
+                                                y0, y1);
+                                    x[i] = __float_as_uint(y0);
+                                    x[i + 1] = __float_as_uint(y1);
+                                }
+                            } else {
+                                const float lo = sTab[piece.lo];
+                                #pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    x[32 * u + i] = __float_as_uint(fmaf(__uint_as_float(x[32 * u + i]), a.scale_log2,
+                                                                         bias_at(lo, hi, i, lane)));
+                            }
                         }
                     }
                 }
@@ -603,6 +627,9 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 m_ref = m_new;
             }
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            if constexpr (BIAS) {
+                if (j + 1 < n) fetch_buckets(j + 1);
+            }
             l_sum += rs;
             // P over the first 64 columns of this tile's S
             tmem_st32(t_lane + s_col, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
@@ -646,6 +673,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                                                 pack_bf16x2(__uint_as_float(u[4]) * inv, __uint_as_float(u[5]) * inv),
                                                 pack_bf16x2(__uint_as_float(u[6]) * inv, __uint_as_float(u[7]) * inv));
                         }
+                        if (a.o_lo) store_remainder(o, inv, static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D + 32 * c);
                     }
                 }
             }
@@ -661,6 +689,10 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             } else {
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D);
                 for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.o_lo) {
+                    uint4 *lo = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D);
+                    for (int e = 0; e < D / 8; ++e) lo[e] = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
         }
     }
@@ -693,7 +725,9 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
     auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention, two tiles)");
     PPArgs a;
     const int positions = TILED ? L.Tp * L.Hp * L.Wp : L.S;
@@ -717,7 +751,9 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.out_f32 = L.out_f32;
     a.stats = L.stats;
     a.lse = L.lse;
-    a.bias_E = L.bias_E;
+    a.o_lo = L.o_lo;
+    a.bias_tab = L.bias_tab;
+    a.buckets = L.buckets;
     a.bias_bm = L.bias_bm;
     a.bias_R = L.bias_R;
     a.n_heads = L.n_heads;
@@ -745,7 +781,7 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
         }
     }
     dim3 grid((a.nq + 1) / 2, L.BH);
-    kern<<<grid, kThreads, C::SMEM, st>>>(maps, a);
+    kern<<<grid, kThreads, smem, st>>>(maps, a);
     return check_cuda(cudaGetLastError(), "attention launch (two tiles)");
 }
 
@@ -999,6 +1035,10 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                     } else {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D);
                         for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+                        if (a.o_lo) {
+                            uint4 *lo = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D);
+                            for (int e = 0; e < D / 8; ++e) lo[e] = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                 }
                 continue;
@@ -1109,6 +1149,7 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                                                 pack_bf16x2(__uint_as_float(u[4]) * inv, __uint_as_float(u[5]) * inv),
                                                 pack_bf16x2(__uint_as_float(u[6]) * inv, __uint_as_float(u[7]) * inv));
                         }
+                        if (a.o_lo) store_remainder(o, inv, static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D + 32 * c);
                     }
                 }
             }
@@ -1176,7 +1217,9 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.out_f32 = L.out_f32;
     a.stats = L.stats;
     a.lse = L.lse;
-    a.bias_E = L.bias_E;
+    a.o_lo = L.o_lo;
+    a.bias_tab = L.bias_tab;
+    a.buckets = L.buckets;
     a.bias_bm = L.bias_bm;
     a.bias_R = L.bias_R;
     a.n_heads = L.n_heads;
@@ -1231,7 +1274,7 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
 }  // namespace
 
 vsa_status launch_attention_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
-    if (L.window && L.bias_E)
+    if (L.window && L.bias_tab)
         return L.D == 128 ? run_pp<128, true, false, false, true>(L, status, st)
                           : run_pp<64, true, false, false, true>(L, status, st);
     if (L.window) return L.D == 128 ? run_pp<128, true, false>(L, status, st) : run_pp<64, true, false>(L, status, st);

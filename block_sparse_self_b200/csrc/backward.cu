@@ -13,7 +13,7 @@ namespace vsa {
 namespace {
 
 struct StatArgs {
-    const void *o, *g;
+    const void *o, *g, *o_lo;
     const float *lse;
     int P, Pw, S_out;
     TileDivs divs[kMaxTiles];
@@ -67,6 +67,15 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
                 for (int c = 0; c < 4; ++c) {
                     o[2 * c] = __uint_as_float(ow[c] << 16);
                     o[2 * c + 1] = __uint_as_float(ow[c] & 0xffff0000u);
+                }
+                if (a.o_lo) {
+                    const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o_lo) + e));
+                    const uint32_t lw[4] = {l4.x, l4.y, l4.z, l4.w};
+                    #pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        o[2 * c] += __uint_as_float(lw[c] << 16);
+                        o[2 * c + 1] += __uint_as_float(lw[c] & 0xffff0000u);
+                    }
                 }
             }
             #pragma unroll
@@ -122,8 +131,8 @@ Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, i
         L.bits = take(transpose_lists_workspace_bytes(lists, nb));
     }
     if (buckets > 0) {
-        L.part = take(BH * (Pw / 128) * 8 * static_cast<size_t>(buckets) * 4);
-        L.bias = take(bias_workspace_bytes(H, S, far));
+        L.part = take(BH * (Pw / 128) * static_cast<size_t>(buckets) * 4);
+        L.bias = take(bias_workspace_bytes(H, S, buckets, far));
     }
     L.total = at;
     return L;
@@ -165,6 +174,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.nlse = f32_at(lay.nlse);
     a.ndelta = f32_at(lay.ndelta);
+    a.ndelta_out = f32_at(lay.ndelta);
     a.none = f32_at(lay.none);
     a.out_f32 = B.grad_f32;
     a.status = status;
@@ -178,6 +188,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
 
     StatArgs s{};
     s.o = B.o;
+    s.o_lo = B.o_lo;
     s.g = B.g;
     s.lse = B.lse;
     s.P = a.P;
@@ -218,7 +229,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
 
     if (buckets > 0) {
         const vsa_status r = check_cuda(launch_bias_expand(B.bias, B.bias_f32, B.H, L.S, buckets, B.far, ws + lay.bias,
-                                                           &a.E, &a.bm, st),
+                                                           &a.tab, &a.bm, st),
                                         "relative bias launch");
         if (r != VSA_OK) return r;
         a.R = bias_reach(L.S, B.far);
@@ -254,7 +265,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     r = launch_bwd_dkv(maps, a, L.D, L.block, L.window, L.tiled, buckets > 0, st);
     if (r != VSA_OK) return r;
     if (a.dbias_part)
-        r = check_cuda(launch_dbias(a.dbias_part, L.BH / B.H, B.H, a.nt * 8, buckets, B.dbias, B.bias_f32, st),
+        r = check_cuda(launch_dbias(a.dbias_part, L.BH / B.H, B.H, a.nt, buckets, B.dbias, B.bias_f32, st),
                        "relative bias gradient launch");
     return r;
 }

@@ -14,6 +14,13 @@
 // so results repeat bit for bit and nothing is accumulated in memory; the
 // price is that S and dP are computed in both passes (7 products instead of
 // 5 per pair of blocks).
+//
+// delta carries the forward pass's roundings of P and o, and one error in
+// delta_i shifts a whole row of dX.  Exactly, sum_j dX_ij = 0; so the dQ pass,
+// which walks whole rows, sums each row of its dX (from delta as it is) and
+// adds the sum to delta_i, and the dK/dV pass, which runs after it, works with
+// the corrected delta.  dbias is summed there for that reason: it adds up many
+// dX of one sign of error.
 #pragma once
 
 #include <math.h>
@@ -39,16 +46,17 @@ struct BwdArgs {
     int half, sink, dense;
     float scale, scale_log2;
     const float *nlse, *ndelta;  // [BH, Pw]: -lse log2e (-inf: the row has no gradient) and -delta
+    float *ndelta_out;           // dQ pass: ndelta with the row sums of dX taken off (see below)
     const float *none;           // 128 values of -inf, then 128 of 0: the statistics of columns past a list's end
     const uint32_t *valid;       // [BH, Pw/32] bits: which positions hold a token; nullptr when all do
     void *d0, *d1;               // dQ pass: dq; dK/dV pass: dk, dv
     int out_f32;
     int *status;
-    // window mode with a bias: E[h][o + R] = log2e bias of offset o (key - query), bm[o + R] its bucket
-    const float *E;
+    // window mode with a bias: tab[h][b] = log2e bias of bucket b, bm[o] = bucket of offset o (key - query), |o| <= R
+    const float *tab;
     const uint8_t *bm;
     int R, buckets;
-    float *dbias_part;  // dQ pass: [BH, nt, 8 warps, buckets]
+    float *dbias_part;  // dK/dV pass: [BH, nt, buckets]
     // tiled mode
     int H2, W2;  // the padded grid's frame
     RealGrid real;

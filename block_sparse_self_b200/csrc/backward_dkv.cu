@@ -15,6 +15,13 @@
 // only reach their own (unwritten) rows; 4 or 2 listed query blocks fill the
 // 128 columns of a tile, and the columns past the list's end repeat its last
 // block with lse = +inf, i.e. P = 0.
+//
+// dbias: dX summed by the bucket of j - i, in fp32 from unrounded values.  A
+// 32 x 32 piece whose offsets share one bucket (most do: buckets widen with
+// distance) adds its row sums to a register, written out when the bucket
+// changes; in the others each warp sums the diagonals by shuffles and then
+// runs of equal buckets.  Every warp has its own partial sums, and all sums
+// have one order.
 #include "backward.cuh"
 
 namespace vsa {
@@ -51,6 +58,8 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
     uint64_t *dv_done = ds_full + 1, *dk_done = dv_done + 1, *mma_done = dk_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *sPart = reinterpret_cast<float *>(tmem_slot + 4);  // BIAS: [8 warps][kMaxBuckets]
+    float *sTab = sPart + 8 * kMaxBuckets;                     // BIAS: [kMaxBuckets]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the leading key blocks of every head first (a sink block is listed by
@@ -67,6 +76,7 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
             kb = a.lead + (id - first) - bh * per;
         }
     }
+    if constexpr (BIAS) bias_table(sTab, a.tab, bh % a.H, a.buckets, threadIdx.x, kBwdThreads);
     int tc = 0;
     bool head_ok = true;
     if constexpr (TILED) {
@@ -264,6 +274,31 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
         const bool rows_live = wq * 32 < BS;          // warp-uniform
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const float sl2 = a.scale_log2;
+        // the bias's gradient: per warp a partial sum for each bucket, and in
+        // registers the sum of the bucket that the last uniform pieces were in
+        [[maybe_unused]] float *part = sPart + warp * kMaxBuckets;
+        [[maybe_unused]] float run_sum[2] = {0.f, 0.f};
+        [[maybe_unused]] int run_bucket[2] = {-1, -1};
+        auto flush = [&](int u) {
+            float t = run_sum[u];
+            #pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == 0 && run_bucket[u] >= 0) part[run_bucket[u]] += t;
+            __syncwarp();
+            run_sum[u] = 0.f;
+        };
+        // buckets of a query tile's three runs of 32 offsets (this lane's of each)
+        [[maybe_unused]] int bk[3] = {0, 0, 0};
+        [[maybe_unused]] auto fetch_buckets = [&](int j) {
+            const int o0 = (kb - qblock(j)) * 128 - 64 * hf + wq * 32 + 32 - lane;
+            #pragma unroll
+            for (int u = 0; u < 3; ++u) bk[u] = bias_bucket(a.bm, a.R, o0 - 32 * u);
+        };
+        if constexpr (BIAS) {
+            for (int b = lane; b < kMaxBuckets; b += 32) part[b] = 0.f;
+            __syncwarp();
+            if (n > 0) fetch_buckets(0);
+        }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (BS < 128 && !rows_live) {  // rows past the block: keep the barriers' phases
@@ -296,6 +331,7 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
             }
             tc_fence_after();
             float pr[64];
+            [[maybe_unused]] BiasPiece piece[2];
             {
                 uint32_t x[64];
                 tmem_ld32(t_lane + C::S_COL + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
@@ -305,8 +341,11 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                 bool masked = false;
                 if constexpr (WINDOW) {
                     const int q0 = qblock(j) * 128, ks = kb * 128;
-                    masked = !(a.dense || ks + 128 <= a.sink || max(q0 + 127 - ks, ks + 127 - q0) <= a.half);
-                    if (masked && p >= a.sink) {
+                    masked = ks + 128 > a.P || !(a.dense || ks + 128 <= a.sink ||
+                                                 max(q0 + 127 - ks, ks + 127 - q0) <= a.half);
+                    if (p >= a.P) {  // no such key: it must not reach dbias
+                        see[0] = see[1] = 0u;
+                    } else if (masked && !a.dense && p >= a.sink) {
                         #pragma unroll
                         for (int u = 0; u < 2; ++u)
                             see[u] = span_bits(q0 + 64 * hf + 32 * u, p - a.half, p + a.half + 1);
@@ -319,20 +358,12 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                         see[u] = group_bits(a, p, qblock(min(j * NSUB + c / BS, count - 1)) * BS + c % BS);
                     }
                 }
-                [[maybe_unused]] float flat = 0.f;
-                [[maybe_unused]] bool uniform = true;
-                [[maybe_unused]] BiasPiece piece[2];
+                [[maybe_unused]] float flat[2] = {0.f, 0.f};
                 if constexpr (BIAS) {
-                    const float *E = a.E + static_cast<size_t>(bh % a.H) * (2 * a.R + 1) + a.R;
-                    const int d = (kb - qblock(j)) * 128;
-                    int bucket;
-                    uniform = bias_uniform(a.bm + a.R, a.R, d, bucket);
-                    if (uniform) {
-                        flat = __ldg(E + min(max(d, -a.R), a.R));
-                    } else {
-                        #pragma unroll
-                        for (int u = 0; u < 2; ++u)
-                            piece[u] = bias_piece(E, a.R, -1, 64 * hf + 32 * u - wq * 32 - d, lane);
+                    #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        piece[u] = bias_piece(bk[u], bk[u + 1]);
+                        if (piece[u].uniform) flat[u] = sTab[piece[u].hi];
                     }
                 }
                 tmem_ld_wait();
@@ -343,16 +374,20 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                 for (int c = 0; c < 64; c += 2) {
                     float y0, y1;
                     uint64_t b = f32x2(nlr[c], nlr[c + 1]);
-                    if constexpr (BIAS) b = add_f32x2(b, f32x2(flat, flat));
+                    if constexpr (BIAS) b = add_f32x2(b, f32x2(flat[c >> 5], flat[c >> 5]));
                     f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, b), y0, y1);
                     x[c] = __float_as_uint(y0);
                     x[c + 1] = __float_as_uint(y1);
                 }
                 if constexpr (BIAS) {
-                    if (!uniform) {
-                        #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(piece[c >> 5], c & 31, lane));
+                    #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (!piece[u].uniform) {
+                            const float lo = sTab[piece[u].lo], hi = sTab[piece[u].hi];
+                            #pragma unroll
+                            for (int c = 32 * u; c < 32 * u + 32; ++c)
+                                x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(lo, hi, c & 31, lane));
+                        }
                     }
                 }
                 if (masked) {
@@ -398,6 +433,13 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                                     y2, y3);
                         dsk[16 * u + 2 * c4] = pack_bf16x2(y0, y1);
                         dsk[16 * u + 2 * c4 + 1] = pack_bf16x2(y2, y3);
+                        if constexpr (BIAS) {
+                            float *q2 = &pr[32 * u + 4 * c4];
+                            q2[0] = y0;
+                            q2[1] = y1;
+                            q2[2] = y2;
+                            q2[3] = y3;
+                        }
                     }
                 }
                 tmem_st32(t_lane + C::DP_COL + 64 * hf, dsk);
@@ -406,8 +448,68 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
+            if constexpr (BIAS) {
+                // the unrounded dX (in pr) by bucket, after the MMA has its operand
+                #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (!a.dbias_part) break;
+                    if (piece[u].uniform) {
+                        if (piece[u].hi != run_bucket[u]) {
+                            flush(u);
+                            run_bucket[u] = piece[u].hi;
+                        }
+                        uint64_t t0 = 0, t1 = 0;  // two pairs of fp32 zeros
+                        #pragma unroll
+                        for (int c = 32 * u; c < 32 * u + 32; c += 4) {
+                            t0 = add_f32x2(t0, f32x2(pr[c], pr[c + 1]));
+                            t1 = add_f32x2(t1, f32x2(pr[c + 2], pr[c + 3]));
+                        }
+                        float a0, a1;
+                        f32x2_split(add_f32x2(t0, t1), a0, a1);
+                        run_sum[u] += a0 + a1;
+                    } else {
+                        // sums of the piece's diagonals: element (r, i) goes to lane (i - r) mod 32
+                        float diag[2] = {0.f, 0.f};  // i - r = lane - 32 and lane
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float v = __shfl_sync(0xffffffffu, pr[32 * u + i], (i - lane) & 31);
+                            if (i >= lane) diag[1] += v;
+                            else diag[0] += v;
+                        }
+                        #pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            // offsets fall with the lane, so equal buckets are neighbours:
+                            // sum each run, its last lane adds to the warp's partial
+                            const int b = m == 0 ? piece[u].lo : piece[u].hi;
+                            float v = diag[m];
+                            #pragma unroll
+                            for (int x = 1; x < 32; x <<= 1) {
+                                const float t = __shfl_up_sync(0xffffffffu, v, x);
+                                const int tb = __shfl_up_sync(0xffffffffu, b, x);
+                                if (lane >= x && tb == b) v += t;
+                            }
+                            const int next = __shfl_down_sync(0xffffffffu, b, 1);
+                            if (lane == 31 || next != b) part[b] += v;
+                            __syncwarp();
+                        }
+                    }
+                }
+                if (j + 1 < n) fetch_buckets(j + 1);
+            }
         }
         if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
+        if constexpr (BIAS) {
+            if (a.dbias_part) {
+                flush(0);
+                flush(1);
+            }
+            named_barrier(1, 256);
+            if (a.dbias_part && static_cast<int>(threadIdx.x) < a.buckets) {
+                float t = 0.f;
+                for (int x = 0; x < 8; ++x) t += sPart[x * kMaxBuckets + threadIdx.x];
+                a.dbias_part[(static_cast<size_t>(bh) * a.nt + kb) * a.buckets + threadIdx.x] = t;
+            }
+        }
 
         // ---- epilogue: warps 0-3 write dV, warps 4-7 dK ----
         const int r = rows_live && row < BS && head_ok ? bwd_row_of<TILED>(p, a, tc) : -1;
@@ -446,9 +548,11 @@ template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     using C = DkvCfg<D>;
     auto kern = bwd_dkv_kernel<D, BS, WINDOW, TILED, BIAS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    constexpr int smem = C::SMEM + (BIAS ? 9 * kMaxBuckets * 4 : 0);
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention backward, dK and dV)");
-    kern<<<static_cast<unsigned>(a.nt) * a.BH, kBwdThreads, C::SMEM, st>>>(maps, a);
+    kern<<<static_cast<unsigned>(a.nt) * a.BH, kBwdThreads, smem, st>>>(maps, a);
     return check_cuda(cudaGetLastError(), "attention backward launch (dK and dV)");
 }
 

@@ -1,7 +1,7 @@
-// backward_dq.cu -- dQ of block-sparse and sliding-window attention, and the
-// gradient of a relative position bias, on tcgen05 tensor cores: one CTA per
-// (query block, batch x head), walking the key blocks of its list (see
-// backward.cuh for the mathematics).
+// backward_dq.cu -- dQ of block-sparse and sliding-window attention on tcgen05
+// tensor cores: one CTA per (query block, batch x head), walking the key blocks
+// of its list (see backward.cuh for the mathematics).  It also corrects delta
+// by the row sums of dX for the dK/dV pass.
 //
 // Queries along the rows: per tile of 128 keys
 //   S = Q K^T, dP = g V^T                  (shared-memory operands)
@@ -11,13 +11,6 @@
 // D = 128: two S buffers, dP and dQ.  dX (bf16) is written over the S it came
 // from, so the next tile's S is computed while this one is worked on, and dP
 // is refilled as soon as it has been read.
-//
-// dbias: dX summed by the bucket of j - i, in fp32 from unrounded values.  A
-// tile whose offsets share one bucket (most do: buckets widen with distance)
-// adds its row sums to one register, written out when the bucket changes; in
-// the others each warp sums its diagonals by shuffles (element (r, i) goes to
-// the lane of its diagonal) and then runs of equal buckets.  Every warp has
-// its own row of partial sums, added in a fixed order by a later kernel.
 #include "backward.cuh"
 
 namespace vsa {
@@ -30,7 +23,7 @@ struct DqCfg {
     static constexpr int NK = D == 128 ? 3 : 4;  // ring of K tiles
     static constexpr int NV = D == 128 ? 2 : 4;  // ring of V tiles
     static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 2 + 4;
-    static constexpr int SMEM = 1024 + (2 + NK + NV) * TILE + N_BARS * 8 + 16;
+    static constexpr int SMEM = 1024 + (2 + NK + NV) * TILE + N_BARS * 8 + 16 + 128 * 4;
     static_assert(SMEM <= 232448, "shared memory");
     static constexpr int DP_COL = 256, DQ_COL = 384;  // S buffers at 0 and 128
 };
@@ -64,9 +57,12 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *list_ok = reinterpret_cast<int *>(tmem_slot + 2);
+    float *sSum = reinterpret_cast<float *>(tmem_slot + 4);  // [128]: row sums of the second half of the columns
+    float *sTab = sSum + 128;                                // BIAS: [kMaxBuckets]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qb = blockIdx.x, bh = blockIdx.y;
+    if constexpr (BIAS) bias_table(sTab, a.tab, bh % a.H, a.buckets, threadIdx.x, kBwdThreads);
     KeyWalk<WINDOW> w{};
     if constexpr (WINDOW) {
         const int q0 = qb * 128;
@@ -275,27 +271,17 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
             nl = __ldg(a.nlse + static_cast<size_t>(bh) * a.Pw + p);
             nd = __ldg(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
         }
-        [[maybe_unused]] float *part = nullptr;
-        [[maybe_unused]] float run_sum = 0.f;
-        [[maybe_unused]] int run_bucket = -1;
-        if constexpr (BIAS) {
-            if (a.dbias_part) {  // null: the table's gradient is not asked for
-                part = a.dbias_part + ((static_cast<size_t>(bh) * a.nt + qb) * 8 + warp) * a.buckets;
-                for (int b = lane; b < a.buckets; b += 32) part[b] = 0.f;
-                __syncwarp();
-            }
-        }
-        // the warp's sum of the current bucket's row sums goes to its partial
-        auto flush = [&]() {
-            if constexpr (BIAS) {
-                float s = run_sum;
-                #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0 && part && run_bucket >= 0) part[run_bucket] += s;
-                __syncwarp();
-                run_sum = 0.f;
-            }
+        float row_sum[2] = {0.f, 0.f};
+        // buckets of a key tile's three runs of 32 offsets (this lane's of each)
+        [[maybe_unused]] int bk[3] = {0, 0, 0};
+        [[maybe_unused]] auto fetch_buckets = [&](int j) {
+            const int o0 = (w.at(j) - qb) * 128 + 64 * hf - wq * 32 - 32 + lane;
+            #pragma unroll
+            for (int u = 0; u < 3; ++u) bk[u] = bias_bucket(a.bm, a.R, o0 + 32 * u);
         };
+        if constexpr (BIAS) {
+            if (n > 0) fetch_buckets(0);
+        }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             if (BS < 128 && !rows_live) {  // rows past the block: keep the barriers' phases
@@ -337,44 +323,41 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
             float pr[64];
-            [[maybe_unused]] bool uniform = true;
-            [[maybe_unused]] int bucket = 0, diag0 = 0;
             {
                 uint32_t x[64];
                 tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
                 tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
-                float y0 = nl;
+                [[maybe_unused]] float flat[2] = {0.f, 0.f};
                 [[maybe_unused]] BiasPiece piece[2];
                 if constexpr (BIAS) {
-                    const float *E = a.E + static_cast<size_t>(bh % a.H) * (2 * a.R + 1) + a.R;
-                    const int d = (w.at(j) - qb) * 128;
-                    uniform = bias_uniform(a.bm + a.R, a.R, d, bucket);
-                    diag0 = d + 64 * hf - wq * 32;  // offset of (row lane 0, column 64 hf)
-                    if (uniform) {
-                        y0 += __ldg(E + min(max(d, -a.R), a.R));
-                    } else {
-                        piece[0] = bias_piece(E, a.R, 1, diag0, lane);
-                        piece[1] = bias_piece(E, a.R, 1, diag0 + 32, lane);
+                    #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        piece[u] = bias_piece(bk[u], bk[u + 1]);
+                        if (piece[u].uniform) flat[u] = sTab[piece[u].hi];
                     }
                 }
                 tmem_ld_wait();
-                const uint64_t sl2x2 = f32x2(sl2, sl2), y0x2 = f32x2(y0, y0);
                 // the exponents, in place; the mask is one branch after all of them, so
                 // that the exponentials below are one straight run
-                // the exponents, in place; the mask is one branch after all of them, so
-                // that the exponentials below are one straight run
+                const uint64_t sl2x2 = f32x2(sl2, sl2);
                 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
+                    const float y0 = BIAS ? nl + flat[c >> 5] : nl;
                     float y[2];
-                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, y0x2), y[0], y[1]);
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2x2, f32x2(y0, y0)),
+                                y[0], y[1]);
                     x[c] = __float_as_uint(y[0]);
                     x[c + 1] = __float_as_uint(y[1]);
                 }
                 if constexpr (BIAS) {
-                    if (!uniform) {
-                        #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(piece[c >> 5], c & 31, lane));
+                    #pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (!piece[u].uniform) {
+                            const float lo = sTab[piece[u].lo], hi = sTab[piece[u].hi];
+                            #pragma unroll
+                            for (int c = 32 * u; c < 32 * u + 32; ++c)
+                                x[c] = __float_as_uint(__uint_as_float(x[c]) + bias_at(lo, hi, c & 31, lane));
+                        }
                     }
                 }
                 if (masked) {
@@ -401,6 +384,8 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
                         f32x2_split(mul_f32x2(f32x2(d0, d1),
                                               add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), ndx2)),
                                     d0, d1);
+                        row_sum[0] += d0;
+                        row_sum[1] += d1;
                         dsk[16 * u + (c >> 1)] = pack_bf16x2(d0, d1);  // bf16: the type of the MMA's operand
                     }
                 }
@@ -411,50 +396,16 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
             __syncwarp();
             if (lane == 0) mbar_arrive(ds_full);
             if constexpr (BIAS) {
-                // sums of the unrounded dX (in pr) by bucket, after the MMA has its operand
-                if (!part) {
-                } else if (uniform) {
-                    if (bucket != run_bucket) {
-                        flush();
-                        run_bucket = bucket;
-                    }
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                    #pragma unroll
-                    for (int c = 0; c < 64; ++c) s[c & 3] += pr[c];
-                    run_sum += (s[0] + s[1]) + (s[2] + s[3]);
-                } else {
-                    // diag[m]: the sum of the diagonal at offset diag0 + 32 (m - 1) + lane
-                    float diag[3] = {0.f, 0.f, 0.f};
-                    #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float v = __shfl_sync(0xffffffffu, pr[32 * u + i], (i - lane) & 31);
-                            if (i >= lane) diag[u + 1] += v;
-                            else diag[u] += v;
-                        }
-                    #pragma unroll
-                    for (int m = 0; m < 3; ++m) {
-                        // offsets rise with the lane, so equal buckets are neighbours:
-                        // sum each run, its last lane adds to the warp's partial
-                        const int o = diag0 + 32 * (m - 1) + lane;
-                        const int b = __ldg(a.bm + a.R + min(max(o, -a.R), a.R));
-                        float v = diag[m];
-                        #pragma unroll
-                        for (int s = 1; s < 32; s <<= 1) {
-                            const float t = __shfl_up_sync(0xffffffffu, v, s);
-                            const int tb = __shfl_up_sync(0xffffffffu, b, s);
-                            if (lane >= s && tb == b) v += t;
-                        }
-                        const int nb = __shfl_down_sync(0xffffffffu, b, 1);
-                        if (lane == 31 || nb != b) part[b] += v;
-                        __syncwarp();
-                    }
-                }
+                if (j + 1 < n) fetch_buckets(j + 1);
             }
         }
         if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
-        flush();
+        // delta + the row's sum of dX, for the dK/dV pass (see backward.cuh)
+        const float mine = row_sum[0] + row_sum[1];
+        if (hf == 1) sSum[row] = mine;
+        named_barrier(1, 256);
+        if (hf == 0 && ok && n > 0 && row < BS && nl != -INFINITY)
+            a.ndelta_out[static_cast<size_t>(bh) * a.Pw + p] = nd - (mine + sSum[row]);
 
         // ---- epilogue: warps 0-3 write the first half of the columns, 4-7 the second ----
         const int r = rows_live && row < BS && head_ok ? bwd_row_of<TILED>(p, a, tc) : -1;
@@ -490,10 +441,12 @@ template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     using C = DqCfg<D>;
     auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention backward, dQ)");
     dim3 grid(a.nt, a.BH);
-    kern<<<grid, kBwdThreads, C::SMEM, st>>>(maps, a);
+    kern<<<grid, kBwdThreads, smem, st>>>(maps, a);
     return check_cuda(cudaGetLastError(), "attention backward launch (dQ)");
 }
 

@@ -417,6 +417,23 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// 32 values x f less their bf16 rounding, rounded to bf16 themselves: with the
+// rounded values they hold x f to 16 significant bits.
+__device__ __forceinline__ void store_remainder(const uint32_t (&x)[32], float f, __nv_bfloat16 *out) {
+    uint4 *dst = reinterpret_cast<uint4 *>(out);
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t r[4];
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float a = __uint_as_float(x[8 * e + 2 * c]) * f, b = __uint_as_float(x[8 * e + 2 * c + 1]) * f;
+            const uint32_t hi = pack_bf16x2(a, b);
+            r[c] = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+        }
+        dst[e] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
 // acc_lo += low bf16 of pk, acc_hi += high bf16 of pk: sm_100 mixed-precision
 // adds (the bf16 operand widens exactly, then one fp32 rounding), with no
 // separate unpacking of the pair.

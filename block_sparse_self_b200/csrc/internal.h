@@ -108,10 +108,13 @@ struct AttnLaunch {
     // optional: per row of o (row r of head bh at lse[bh * S + r]) the natural
     // logarithm of the sum behind its softmax, -inf where no key was seen
     float *lse;
-    // window mode, optional: relative position bias by offset (relative_bias.cu)
-    const float *bias_E;
+    // optional, for a bf16 o: [BH, S, D] bf16, what o's rounding left (rows of
+    // zeros where o is zeros)
+    void *o_lo;
+    // window mode, optional: relative position bias (relative_bias.cu)
+    const float *bias_tab;
     const uint8_t *bias_bm;
-    int bias_R, n_heads;
+    int bias_R, buckets, n_heads;
 };
 vsa_status launch_attention(const AttnLaunch &a, int *status, cudaStream_t st);
 // Two query tiles per CTA (128-token blocks only); launch_attention routes to it.
@@ -146,12 +149,13 @@ size_t transpose_lists_workspace_bytes(int lists, int nb);
 cudaError_t launch_transpose_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap, int32_t *offsets,
                                    int32_t *rows, bool fill, void *workspace, int *status, cudaStream_t st);
 
-// Relative position bias (relative_bias.cu): values by offset -R .. R, R =
-// bias_reach(S, far), in the workspace; bucket numbers; the gradient's last sum.
+// Relative position bias (relative_bias.cu): values by head and bucket, and the
+// buckets of offsets -R .. R, R = bias_reach(S, far), in the workspace (*bm at
+// offset 0); bucket numbers; the gradient's last sum.
 int bias_reach(int S, int far);
-size_t bias_workspace_bytes(int H, int S, int far);
+size_t bias_workspace_bytes(int H, int S, int buckets, int far);
 cudaError_t launch_bias_expand(const void *table, bool f32, int H, int S, int buckets, int far, void *workspace,
-                               const float **E, const uint8_t **bm, cudaStream_t st);
+                               const float **tab, const uint8_t **bm, cudaStream_t st);
 cudaError_t launch_bias_buckets(int buckets, int far, int32_t *out, cudaStream_t st);
 cudaError_t launch_dbias(const float *part, int B, int H, int per, int buckets, void *dtable, bool f32,
                          cudaStream_t st);
@@ -161,6 +165,7 @@ cudaError_t launch_dbias(const float *part, int B, int H, int per, int buckets, 
 struct BackwardLaunch {
     AttnLaunch a;
     const void *g, *o;   // dL/do (bf16) and the forward output
+    const void *o_lo;    // what o's rounding to bf16 left, or nullptr
     int o_f32;
     const float *lse;
     void *dq, *dk, *dv;

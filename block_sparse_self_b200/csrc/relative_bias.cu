@@ -8,9 +8,9 @@
 // e (far / e)^(t / (n - e)); those borders are rounded up to whole numbers on
 // the host, so the kernels only compare integers.
 //
-// The attention kernels read the bias by offset: E[h][r + R] = log2(e)
-// table[bucket(r)][h] for |r| <= R, R = min(far, S) (larger offsets fall into
-// the last bucket of their side).  E is a few KB to a few MB and stays in L2.
+// The attention kernels read bucket(r) as a byte, for |r| <= R = min(far, S)
+// (larger offsets fall into the last bucket of their side), and each head's
+// values tab[h][b] = log2(e) table[b][h].
 #include "common.cuh"
 #include "internal.h"
 
@@ -53,18 +53,18 @@ __global__ void buckets_kernel(const Borders b, int far, int32_t *__restrict__ o
 }
 
 template <typename T>
-__global__ void expand_kernel(const Borders b, const T *__restrict__ table, int H, int R, float *__restrict__ E,
-                              uint8_t *__restrict__ bm) {
-    const int x = blockIdx.x * 256 + threadIdx.x, h = blockIdx.y;
-    if (x > 2 * R) return;
-    const int k = bucket_of(x - R, b);
-    E[static_cast<size_t>(h) * (2 * R + 1) + x] =
-        static_cast<float>(table[static_cast<size_t>(k) * H + h]) * 1.4426950408889634f;
-    if (h == 0) bm[x] = static_cast<uint8_t>(k);
+__global__ void expand_kernel(const Borders b, const T *__restrict__ table, int H, int buckets, int R,
+                              float *__restrict__ tab, uint8_t *__restrict__ bm) {
+    const int x = blockIdx.x * 256 + threadIdx.x;
+    if (x <= 2 * R) bm[x] = static_cast<uint8_t>(bucket_of(x - R, b));
+    if (x < H * buckets) {
+        const int h = x / buckets, k = x - h * buckets;
+        tab[x] = static_cast<float>(table[static_cast<size_t>(k) * H + h]) * 1.4426950408889634f;
+    }
 }
 
 // dtable[b][h]: the partial sums [B, H, per, buckets] over the batch and the
-// warps of every query tile, in a fixed order and in 64 bits.
+// key tiles, in a fixed order and in 64 bits.
 template <typename T>
 __global__ void __launch_bounds__(1024) dbias_kernel(const float *__restrict__ part, int B, int H, int per, int buckets,
                                                      T *__restrict__ dtable) {
@@ -90,25 +90,23 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int bias_reach(int S, int far) { return far < S ? far : S; }
 
-size_t bias_workspace_bytes(int H, int S, int far) {
-    const size_t n = 2 * static_cast<size_t>(bias_reach(S, far)) + 1;
-    return up256(static_cast<size_t>(H) * n * 4) + up256(n);
+size_t bias_workspace_bytes(int H, int S, int buckets, int far) {
+    return up256(static_cast<size_t>(H) * buckets * 4) + up256(2 * static_cast<size_t>(bias_reach(S, far)) + 1);
 }
 
 cudaError_t launch_bias_expand(const void *table, bool f32, int H, int S, int buckets, int far, void *workspace,
-                               const float **E, const uint8_t **bm, cudaStream_t st) {
+                               const float **tab, const uint8_t **bm, cudaStream_t st) {
     const int R = bias_reach(S, far);
-    const size_t n = 2 * static_cast<size_t>(R) + 1;
-    float *e = static_cast<float *>(workspace);
-    uint8_t *m = static_cast<uint8_t *>(workspace) + up256(static_cast<size_t>(H) * n * 4);
+    float *t = static_cast<float *>(workspace);
+    uint8_t *m = static_cast<uint8_t *>(workspace) + up256(static_cast<size_t>(H) * buckets * 4);
     const Borders b = make_borders(buckets, far);
-    const dim3 grid(static_cast<unsigned>((n + 255) / 256), H);
+    const int n = 2 * R + 1 > H * buckets ? 2 * R + 1 : H * buckets;
     if (f32)
-        expand_kernel<<<grid, 256, 0, st>>>(b, static_cast<const float *>(table), H, R, e, m);
+        expand_kernel<<<(n + 255) / 256, 256, 0, st>>>(b, static_cast<const float *>(table), H, buckets, R, t, m);
     else
-        expand_kernel<<<grid, 256, 0, st>>>(b, static_cast<const __nv_bfloat16 *>(table), H, R, e, m);
-    *E = e;
-    *bm = m;
+        expand_kernel<<<(n + 255) / 256, 256, 0, st>>>(b, static_cast<const __nv_bfloat16 *>(table), H, buckets, R, t, m);
+    *tab = t;
+    *bm = m + R;  // offset 0
     return cudaGetLastError();
 }
 

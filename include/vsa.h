@@ -469,7 +469,10 @@ vsa_status vsa_head_profile(const void *q, const void *k, int B, int n_heads, in
  * The forward calls with _lse in their names are the calls above with one
  * more output, lse [B, n_heads, S] fp32: per row of o the natural logarithm
  * of the sum behind its softmax (-inf for a row that saw no key, whose o is
- * zero).  o is the same bit for bit.
+ * zero).  o is the same bit for bit.  o_lo (NULL, or [B, n_heads, S, D] bf16
+ * beside a bf16 o) receives what rounding o to bf16 left; given to the
+ * backward call it makes delta below as exact as an fp32 o would, which dq
+ * and dbias gain from.
  *
  * With x_ij = scale q_i . k_j (+ bias) over the keys row i sees,
  * P_ij = exp(x_ij - lse_i), g = dL/do and delta_i = g_i . o_i:
@@ -483,18 +486,18 @@ vsa_status vsa_head_profile(const void *q, const void *k, int B, int n_heads, in
  * that is computed has weight zero, and zero times a non-finite q, k, v or
  * dout of that block is NaN; blocks that no list names are not read.
  *   dout       [B, n_heads, S, D] bf16, in the order of o
- *   o, lse     as the forward call wrote them, o in o_dtype
+ *   o, o_lo, lse as the forward call wrote them, o in o_dtype; o_lo or NULL
  *   dq, dk, dv [B, n_heads, S, D] in grad_dtype, in the order of q, k and v
  *   workspace  DEVICE scratch of the _workspace_size call's bytes, 256-byte
  *              aligned, one per call in flight
  * Outputs and workspace must not overlap one another or an input.  All other
  * arguments as in the forward call.                                         */
 vsa_status vsa_block_sparse_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
-                                          float *lse, int B, int n_heads, int S, int D, int block, const int32_t *idx,
+                                          float *lse, void *o_lo, int B, int n_heads, int S, int D, int block, const int32_t *idx,
                                           const int32_t *cnt, int cap, int list_per_head, int group_size, float scale,
                                           void *stream);
 vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, const void *v, void *o,
-                                                vsa_dtype out_dtype, float *lse, int B, int n_heads, int S, int D,
+                                                vsa_dtype out_dtype, float *lse, void *o_lo, int B, int n_heads, int S, int D,
                                                 vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
                                                 const int32_t *choice, const int32_t *idx, const int32_t *cnt, int cap,
                                                 int list_per_head, int group_stride, float scale, void *stream);
@@ -504,13 +507,13 @@ vsa_status vsa_block_sparse_attention_tiled_lse(const void *q, const void *k, co
 size_t vsa_block_sparse_attention_backward_workspace_size(int B, int n_heads, int positions, int block, int cap,
                                                           int list_per_head);
 vsa_status vsa_block_sparse_attention_backward(const void *dout, const void *q, const void *k, const void *v,
-                                               const void *o, vsa_dtype o_dtype, const float *lse, void *dq, void *dk,
+                                               const void *o, vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq, void *dk,
                                                void *dv, vsa_dtype grad_dtype, int B, int n_heads, int S, int D,
                                                int block, const int32_t *idx, const int32_t *cnt, int cap,
                                                int list_per_head, int group_size, float scale, void *workspace,
                                                size_t workspace_bytes, void *stream);
 vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const void *q, const void *k, const void *v,
-                                                     const void *o, vsa_dtype o_dtype, const float *lse, void *dq,
+                                                     const void *o, vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq,
                                                      void *dk, void *dv, vsa_dtype grad_dtype, int B, int n_heads,
                                                      int S, int D, vsa_dims3 grid, const vsa_dims3 *tiles, int n_tiles,
                                                      const int32_t *choice, const int32_t *idx, const int32_t *cnt,
@@ -538,12 +541,12 @@ vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const voi
  *              vsa_window_attention_backward_workspace_size bytes             */
 size_t vsa_window_attention_lse_workspace_size(int n_heads, int S, int num_buckets, int max_distance);
 vsa_status vsa_window_attention_lse(const void *q, const void *k, const void *v, void *o, vsa_dtype out_dtype,
-                                    float *lse, int B, int n_heads, int S, int D, int window, int sink, float scale,
+                                    float *lse, void *o_lo, int B, int n_heads, int S, int D, int window, int sink, float scale,
                                     const void *bias, vsa_dtype bias_dtype, int num_buckets, int max_distance,
                                     void *workspace, size_t workspace_bytes, void *stream);
 size_t vsa_window_attention_backward_workspace_size(int B, int n_heads, int S, int num_buckets, int max_distance);
 vsa_status vsa_window_attention_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
-                                         vsa_dtype o_dtype, const float *lse, void *dq, void *dk, void *dv,
+                                         vsa_dtype o_dtype, const void *o_lo, const float *lse, void *dq, void *dk, void *dv,
                                          vsa_dtype grad_dtype, int B, int n_heads, int S, int D, int window, int sink,
                                          float scale, const void *bias, vsa_dtype bias_dtype, int num_buckets,
                                          int max_distance, void *dbias, void *workspace, size_t workspace_bytes,

@@ -485,8 +485,9 @@ def test_autograd_matches_the_functions(dtype):
     leaves = [x.clone().requires_grad_() for x in (q, k, v)]
     o = vsa.block_sparse_attention(*leaves, idx, cnt, 128)
     with torch.no_grad():
-        o2, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, 128, return_lse=True)
-        want = vsa.block_sparse_attention_backward(g, q, k, v, o2, lse, idx, cnt, 128)
+        o2, lse, o_lo = vsa.block_sparse_attention(q, k, v, idx, cnt, 128, return_remainder=True)
+        want = vsa.block_sparse_attention_backward(g, q, k, v, o2, lse, idx, cnt, 128, o_lo=o_lo)
+        assert (o_lo is None) == (dtype == torch.float32)
     assert torch.equal(o, o2) and o.dtype == dtype
     got = torch.autograd.grad(o, leaves, g)
     for x, y in zip(got, want):
@@ -494,7 +495,7 @@ def test_autograd_matches_the_functions(dtype):
     # an expanded gradient (a sum's) and a backward pass for one leaf alone
     o = vsa.block_sparse_attention(q, leaves[1], v, idx, cnt, 128)
     o.sum().backward()
-    ones = vsa.block_sparse_attention_backward(torch.ones_like(o), q, k, v, o2, lse, idx, cnt, 128)
+    ones = vsa.block_sparse_attention_backward(torch.ones_like(o), q, k, v, o2, lse, idx, cnt, 128, o_lo=o_lo)
     assert torch.equal(leaves[1].grad, ones[1]) and q.grad is None
 
 
@@ -595,6 +596,36 @@ def test_captured_and_on_another_stream():
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("mode", ["lists", "lists64", "one", "tiled", "window", "bias"])
+def test_remainder(mode):
+    """o + o_lo is the fp32 output to 16 bits, and the gradients are those from the fp32 output to the same."""
+    D, H, S = 64, 2, 512
+    q, k, v, g = inputs(1, H, S, D, seed=21)
+    block = 64 if mode == "lists64" else 128
+    idx, cnt = random_lists(1, H, S // block, 1 if mode == "one" else 3, seed=21)
+    if mode == "tiled":
+        fwd, bwd, args, kw = (vsa.block_sparse_attention_tiled, vsa.block_sparse_attention_tiled_backward,
+                              ((4, 8, 16), [(1, 8, 16)], None, idx, cnt), {})
+    elif mode in ("window", "bias"):
+        fwd, bwd, args = vsa.window_attention, vsa.window_attention_backward, (200, 9)
+        kw = dict(bias=torch.randn(32, H, device=DEV)) if mode == "bias" else {}
+    else:
+        fwd, bwd, args, kw = vsa.block_sparse_attention, vsa.block_sparse_attention_backward, (idx, cnt, block), {}
+    o, lse, o_lo = fwd(q, k, v, *args, return_remainder=True, **kw)
+    full, lse2 = fwd(q, k, v, *args, out_dtype=torch.float32, return_lse=True, **kw)
+    assert torch.equal(o, full.bfloat16()) and torch.equal(lse, lse2)
+    # the remainder is at most u |o| and rounded by u of itself
+    assert ((o.double() + o_lo.double() - full.double()).abs() <= U * U * full.double().abs()).all()
+    low = bwd(g, q, k, v, o, lse, *args, o_lo=o_lo, grad_dtype=torch.float32, **kw)
+    want = bwd(g, q, k, v, full, lse, *args, grad_dtype=torch.float32, **kw)
+    rough = bwd(g, q, k, v, o, lse, *args, grad_dtype=torch.float32, **kw)
+    for x, y, z in zip(low[:3], want, rough):
+        # delta differs by u^2 |g||o| where a bf16 o alone would leave u |g||o|; dX and P are rounded alike, so
+        # few of their roundings change: u of the gradient's norm is far above what is left
+        assert (x - y).norm() <= U / 4 * y.norm()
+        assert (z - y).norm() <= 4 * U * y.norm()
+
+
 def test_bias_without_its_gradient():
     q, k, v, g = inputs(1, 2, 300, 64, seed=14)
     bias = torch.randn(32, 2, device=DEV)
@@ -605,8 +636,9 @@ def test_bias_without_its_gradient():
     for x, y in zip(a[:3], b[:3]):
         assert torch.equal(x, y)
     leaf = q.clone().requires_grad_()
-    o = vsa.window_attention(leaf, k, v, 64, bias=bias)
-    assert torch.equal(torch.autograd.grad(o, leaf, g)[0], a[0])
+    o, _, o_lo = vsa.window_attention(leaf, k, v, 64, bias=bias, return_remainder=True)
+    want = vsa.window_attention_backward(g, q, k, v, o.detach(), lse, 64, bias=bias, bias_grad=False, o_lo=o_lo)
+    assert torch.equal(torch.autograd.grad(o, leaf, g)[0], want[0])
 
 
 def test_refusals():
