@@ -14,6 +14,7 @@ RuntimeError, unsupported-but-valid requests raise NotImplementedError.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -125,12 +126,23 @@ def _check(status: int) -> None:
     raise RuntimeError(msg)
 
 
-def _stream(device=None) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device=None) -> int:
+    """The raw handle of the device's current stream (without the Stream object that
+    torch.cuda.current_stream makes: a tenth of the time, which small calls notice)."""
+    index = torch.cuda.current_device() if device is None or device.index is None else device.index
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _on(t: torch.Tensor):
+    """Makes t's device current for the calls inside, if it is not."""
+    return _NO_GUARD if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+_NO_GUARD = contextlib.nullcontext()
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -587,10 +599,11 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     if return_lse or return_remainder:
         lse, o_lo = _saved_outputs(o, return_remainder)
-        _check(lib().vsa_block_sparse_attention_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse),
-                                                    _ptr(o_lo), B, H, S, D, int(block), _ptr(idx), _ptr(cnt), int(cap),
-                                                    1 if per_head else 0, int(group_size), _scale(scale),
-                                                    _stream(q.device)))
+        with _on(q):
+            _check(lib().vsa_block_sparse_attention_lse(
+                _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), _ptr(o_lo), B, H, S, D, int(block),
+                _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size), _scale(scale),
+                _stream(q.device)))
         return _saved(o, lse, o_lo, return_lse, return_remainder)
     _check(lib().vsa_block_sparse_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(block),
                                             _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size),
@@ -613,7 +626,7 @@ def block_sparse_attention_backward(do, q, k, v, o, lse, idx, cnt, block: int, g
     _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt)
     cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
-    with torch.cuda.device(q.device):
+    with _on(q):
         need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, S, int(block), cap, per_head)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         _check(lib().vsa_block_sparse_attention_backward(
@@ -636,9 +649,9 @@ def transpose_block_lists(idx, cnt):
     lists = math.prod(lead)
     offsets = torch.empty(*lead, nb + 1, dtype=torch.int32, device=idx.device)
     rows = torch.empty(*lead, nb * cap, dtype=torch.int32, device=idx.device)
-    with torch.cuda.device(idx.device):
+    with _on(idx):
         need = lib().vsa_transpose_block_lists_workspace_size(lists, nb)
-        ws = torch.empty(need, dtype=torch.uint8, device=idx.device)
+        ws = torch.empty(need, dtype=torch.uint8, device=idx.device) if need else None
         _check(lib().vsa_transpose_block_lists(_ptr(idx), _ptr(cnt), lists, nb, cap, _ptr(offsets), _ptr(rows),
                                                _ptr(ws), need, _stream(idx.device)))
     return offsets, rows
@@ -725,8 +738,9 @@ def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: 
             1 if idx.dim() == 4 else 0, int(group_stride), _scale(scale), _stream(q.device))
     if return_lse or return_remainder:
         lse, o_lo = _saved_outputs(o, return_remainder)
-        _check(lib().vsa_block_sparse_attention_tiled_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse),
-                                                          _ptr(o_lo), *tail))
+        with _on(q):
+            _check(lib().vsa_block_sparse_attention_tiled_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt),
+                                                              _ptr(lse), _ptr(o_lo), *tail))
         return _saved(o, lse, o_lo, return_lse, return_remainder)
     _check(lib().vsa_block_sparse_attention_tiled(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), *tail))
     return o
@@ -750,7 +764,7 @@ def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choi
     _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt, choice=choice)
     cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
-    with torch.cuda.device(q.device):
+    with _on(q):
         need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, positions, block, cap, per_head)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         _check(lib().vsa_block_sparse_attention_tiled_backward(
@@ -838,7 +852,7 @@ def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float]
     lse, o_lo = _saved_outputs(o, return_remainder) if return_lse or return_remainder else (None, None)
     buckets, need, ws = 0, 0, None
     _same_device(q, k=k, v=v, bias=bias)
-    with torch.cuda.device(q.device):
+    with _on(q):
         if bias is not None:
             buckets = _bias_arg(bias, H)
             need = lib().vsa_window_attention_lse_workspace_size(H, S, buckets, int(max_distance))
@@ -864,7 +878,7 @@ def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, s
     buckets = 0 if bias is None else _bias_arg(bias, H)
     dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
     dbias = None if bias is None or not bias_grad else torch.empty_like(bias)
-    with torch.cuda.device(q.device):
+    with _on(q):
         need = lib().vsa_window_attention_backward_workspace_size(B, H, S, buckets, int(max_distance))
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
         _check(lib().vsa_window_attention_backward(
@@ -879,7 +893,7 @@ def relative_position_buckets(num_buckets: int, max_distance: int, device="cuda"
     """int32 [2 * max_distance + 1]: the bucket of each relative position (key - query) from
     -max_distance to max_distance (see window_attention and include/vsa.h)."""
     out = torch.empty(max(1, 2 * int(max_distance) + 1), dtype=torch.int32, device=device)
-    with torch.cuda.device(out.device):
+    with _on(out):
         _check(lib().vsa_relative_position_buckets(int(num_buckets), int(max_distance), _ptr(out), _stream(out.device)))
     return out
 

@@ -869,14 +869,14 @@ vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int
     VSA_REQUIRE(aligned4(idx) && aligned4(cnt), "idx and cnt must be non-NULL 4-byte aligned device pointers");
     VSA_REQUIRE(aligned4(offsets) && aligned4(rows), "offsets and rows must be non-NULL 4-byte aligned device pointers");
     const size_t need = vsa_transpose_block_lists_workspace_size(lists, nb);
-    VSA_TRY(check_workspace(workspace, workspace_bytes, need));
+    if (need > 0) VSA_TRY(check_workspace(workspace, workspace_bytes, need));
     const size_t n_idx = static_cast<size_t>(lists) * nb * cap * 4, n_cnt = static_cast<size_t>(lists) * nb * 4,
                  n_off = static_cast<size_t>(lists) * (nb + 1) * 4;
     VSA_REQUIRE(!overlaps(offsets, n_off, idx, n_idx) && !overlaps(offsets, n_off, cnt, n_cnt) &&
                     !overlaps(rows, n_idx, idx, n_idx) && !overlaps(rows, n_idx, cnt, n_cnt) &&
-                    !overlaps(rows, n_idx, offsets, n_off) && !overlaps(workspace, need, idx, n_idx) &&
-                    !overlaps(workspace, need, cnt, n_cnt) && !overlaps(workspace, need, offsets, n_off) &&
-                    !overlaps(workspace, need, rows, n_idx),
+                    !overlaps(rows, n_idx, offsets, n_off) &&
+                    (need == 0 || (!overlaps(workspace, need, idx, n_idx) && !overlaps(workspace, need, cnt, n_cnt) &&
+                                   !overlaps(workspace, need, offsets, n_off) && !overlaps(workspace, need, rows, n_idx))),
                 "offsets, rows and workspace must not overlap one another, idx or cnt");
     return check_cuda(launch_transpose_lists(idx, cnt, lists, nb, cap, offsets, rows, true, workspace,
                                              status_or_null(stream), as_stream(stream)),

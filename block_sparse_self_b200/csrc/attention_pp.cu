@@ -519,12 +519,17 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                     const bool full = (ks + BN <= S) &&
                                       (a.dense || ks + BN <= a.sink || max(qe - 1 - ks, ks + BN - 1 - q0) <= a.half);
                     if (!full) {
+                        // the row's visible columns as bits: testing each column's conditions
+                        // in turn branched several times per element (36.7 us against 12.9 for
+                        // a window of 100 over S = 517, D = 64)
                         #pragma unroll
-                        for (int c = 0; c < BN; ++c) {
-                            const int kc2 = ks + c;
-                            const int dd = rg > kc2 ? rg - kc2 : kc2 - rg;
-                            if (!(kc2 < S && (a.dense || kc2 < a.sink || dd <= a.half)))
-                                x[c] = __float_as_uint(-INFINITY);
+                        for (int u = 0; u < BN / 32; ++u) {
+                            const int c0 = ks + 32 * u;
+                            uint32_t see = span_bits(c0, 0, S);
+                            if (!a.dense) see &= span_bits(c0, rg - a.half, rg + a.half + 1) | span_bits(c0, 0, a.sink);
+                            #pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((see >> c) & 1u)) x[32 * u + c] = __float_as_uint(-INFINITY);
                         }
                     }
                 } else {

@@ -46,51 +46,62 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     if (a.valid && lane == 0) a.valid[static_cast<size_t>(bh) * (a.Pw / 32) + p0 / 32] = bits;
     const int sub = lane / LPR, at = lane % LPR;
     float delta = 0.f;
-    #pragma unroll 4
-    for (int r0 = 0; r0 < 32; r0 += ROWS) {
-        const int rt = __shfl_sync(0xffffffffu, tok, r0 + sub);
-        float s = 0.f;
-        if (rt >= 0) {
+    // eight groups of rows at a time: all their loads first (rows without a
+    // token load the head's first row and count as zero)
+    constexpr int U = 8;
+    static_assert(32 % (U * ROWS) == 0, "groups of rows");
+    #pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += U * ROWS) {
+        uint4 gv[U], ov[U], lv[U];
+        [[maybe_unused]] uint4 ow[U];  // fp32 o: the second four of a lane's eight values
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int rt = max(__shfl_sync(0xffffffffu, tok, r0 + u * ROWS + sub), 0);
             const size_t e = (static_cast<size_t>(bh) * a.S_out + rt) * D + at * 8;
-            const uint4 g4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.g) + e));
-            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+            gv[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.g) + e));
+            if constexpr (O_F32) {
+                ov[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(a.o) + e));
+                ow[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(a.o) + e + 4));
+            } else {
+                ov[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + e));
+                lv[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.o_lo) lv[u] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o_lo) + e));
+            }
+        }
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t gw[4] = {gv[u].x, gv[u].y, gv[u].z, gv[u].w};
+            const uint32_t x[4] = {ov[u].x, ov[u].y, ov[u].z, ov[u].w};
             float o[8];
             if constexpr (O_F32) {
-                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(a.o) + e);
-                const float4 x = __ldg(src), y = __ldg(src + 1);
-                o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-                o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
-            } else {
-                const uint4 o4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o) + e));
-                const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
+                const uint32_t y[4] = {ow[u].x, ow[u].y, ow[u].z, ow[u].w};
                 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    o[2 * c] = __uint_as_float(ow[c] << 16);
-                    o[2 * c + 1] = __uint_as_float(ow[c] & 0xffff0000u);
+                    o[c] = __uint_as_float(x[c]);
+                    o[c + 4] = __uint_as_float(y[c]);
                 }
-                if (a.o_lo) {
-                    const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.o_lo) + e));
-                    const uint32_t lw[4] = {l4.x, l4.y, l4.z, l4.w};
-                    #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        o[2 * c] += __uint_as_float(lw[c] << 16);
-                        o[2 * c + 1] += __uint_as_float(lw[c] & 0xffff0000u);
-                    }
+            } else {
+                const uint32_t y[4] = {lv[u].x, lv[u].y, lv[u].z, lv[u].w};
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    o[2 * c] = __uint_as_float(x[c] << 16) + __uint_as_float(y[c] << 16);
+                    o[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u) + __uint_as_float(y[c] & 0xffff0000u);
                 }
             }
+            float s = 0.f;
             #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 s = fmaf(__uint_as_float(gw[c] << 16), o[2 * c], s);
                 s = fmaf(__uint_as_float(gw[c] & 0xffff0000u), o[2 * c + 1], s);
             }
-        }
-        #pragma unroll
-        for (int x = LPR / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        // lane r0 + u keeps row r0 + u's sum, held by the lanes of group u
-        #pragma unroll
-        for (int u = 0; u < ROWS; ++u) {
-            const float v = __shfl_sync(0xffffffffu, s, u * LPR);
-            if (lane == r0 + u) delta = v;
+            #pragma unroll
+            for (int m = LPR / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            // lane r0 + u ROWS + v keeps that row's sum, held by the lanes of group v
+            #pragma unroll
+            for (int v = 0; v < ROWS; ++v) {
+                const float t = __shfl_sync(0xffffffffu, s, v * LPR);
+                if (lane == r0 + u * ROWS + v) delta = t;
+            }
         }
     }
     float nl = -INFINITY;
@@ -100,7 +111,7 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
         // softmax to differentiate; NaN lets the gradients show it.
         nl = l == -INFINITY ? -INFINITY : l == INFINITY ? NAN : -l * 1.4426950408889634f;
     }
-    if (nl == -INFINITY) delta = 0.f;
+    if (nl == -INFINITY) delta = 0.f;  // also a row that holds no token
     const size_t out = static_cast<size_t>(bh) * a.Pw + p;
     a.nlse[out] = nl;
     a.ndelta[out] = -delta;

@@ -122,13 +122,6 @@ __device__ __forceinline__ int bwd_row_of(int p, const BwdArgs &a, int tc) {
     return p;
 }
 
-// Bits [lo, hi) of the 32 columns that start at `base`.
-__device__ __forceinline__ uint32_t span_bits(int base, int lo, int hi) {
-    const int x = min(max(lo - base, 0), 32), y = min(max(hi - base, 0), 32);
-    const uint32_t below_y = y >= 32 ? ~0u : (1u << y) - 1u, below_x = x >= 32 ? ~0u : (1u << x) - 1u;
-    return below_y & ~below_x;
-}
-
 // Columns base .. base + 31 that share row position p's group (both kinds of
 // groups are symmetric, so the same bits serve queries and keys as rows).
 __device__ __forceinline__ uint32_t group_bits(const BwdArgs &a, int p, int base) {

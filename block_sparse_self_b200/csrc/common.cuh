@@ -401,6 +401,13 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Bits [lo, hi) of the 32 columns that start at `base`.
+__device__ __forceinline__ uint32_t span_bits(int base, int lo, int hi) {
+    const int x = min(max(lo - base, 0), 32), y = min(max(hi - base, 0), 32);
+    const uint32_t below_y = y >= 32 ? ~0u : (1u << y) - 1u, below_x = x >= 32 ? ~0u : (1u << x) - 1u;
+    return below_y & ~below_x;
+}
+
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

@@ -563,6 +563,8 @@ vsa_status vsa_relative_position_buckets(int num_buckets, int max_distance, int3
  *   offsets   [lists, nb + 1]: key block j's query blocks are
  *             rows[offsets[j] .. offsets[j + 1])
  *   rows      [lists, nb * cap], -1 behind the last entry
+ *   workspace DEVICE scratch of the _workspace_size call's bytes, 256-byte
+ *             aligned; NULL will do where that is 0 (nb <= 128)
  * A query block whose list breaks these rules appears nowhere and sets
  * VSA_ERR_RUNTIME.  nb * cap < 2^31.                                        */
 size_t vsa_transpose_block_lists_workspace_size(int lists, int nb);

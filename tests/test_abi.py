@@ -353,3 +353,117 @@ def test_header_is_plain_c(tmp_path):
         r = subprocess.run([compiler, std, "-Wall", "-Werror", "-fsyntax-only", *lang, str(src)],
                            capture_output=True, text=True)
         assert r.returncode == 0, r.stderr
+
+
+# ---- training: forward passes with lse, backward passes, bias, transposed lists ----
+
+def _at(n):
+    """The n-th of a row of fake 16 MB buffers that do not overlap."""
+    return ctypes.c_void_p((n + 1) << 24)
+
+
+def test_lse_argument_errors(L):
+    def call(**kw):
+        a = dict(lse=_at(4), o_lo=NULL, out=vsa.BF16, block=32, o=_at(3))
+        a.update(kw)
+        return L.vsa_block_sparse_attention_lse(_at(0), _at(1), _at(2), a["o"], a["out"], a["lse"], a["o_lo"], 1, 2,
+                                                256, 64, a["block"], _at(6), _at(7), 4, 1, 0, 0.0, NULL)
+    assert call(lse=NULL) == vsa.ERR_INVALID_ARGUMENT and "lse" in vsa.last_error()
+    assert call(lse=_at(3)) == vsa.ERR_INVALID_ARGUMENT          # overlaps o
+    assert call(o_lo=_at(1)) == vsa.ERR_INVALID_ARGUMENT         # overlaps k
+    assert call(o_lo=_at(4)) == vsa.ERR_INVALID_ARGUMENT         # overlaps lse
+    assert call(o_lo=_at(5), out=vsa.F32) == vsa.ERR_INVALID_ARGUMENT
+    assert "remainder" in vsa.last_error() or "rounding" in vsa.last_error()
+    assert call(o_lo=MIS) == vsa.ERR_INVALID_ARGUMENT
+    assert call(block=48) == vsa.ERR_INVALID_ARGUMENT
+
+
+def test_block_sparse_backward_argument_errors(L):
+    need = L.vsa_block_sparse_attention_backward_workspace_size(1, 2, 256, 64, 4, 1)
+    assert need > 0 and need % 256 == 0
+    for bad in ((0, 2, 256, 64, 4, 1), (1, 2, 250, 64, 4, 1), (1, 2, 256, 48, 4, 1), (1, 2, 256, 64, 0, 1)):
+        assert L.vsa_block_sparse_attention_backward_workspace_size(*bad) == 0
+
+    def call(**kw):
+        a = dict(g=_at(0), o=_at(4), lse=_at(5), dq=_at(6), dk=_at(7), dv=_at(8), grad=vsa.BF16, odt=vsa.BF16,
+                 o_lo=NULL, ws=_at(9), bytes=need, D=64, S=256, block=64, cap=4, scale=0.0)
+        a.update(kw)
+        return L.vsa_block_sparse_attention_backward(
+            a["g"], _at(1), _at(2), _at(3), a["o"], a["odt"], a["o_lo"], a["lse"], a["dq"], a["dk"], a["dv"],
+            a["grad"], 1, 2, a["S"], a["D"], a["block"], _at(10), _at(11), a["cap"], 1, 0, a["scale"], a["ws"],
+            a["bytes"], NULL)
+    for kw in (dict(g=NULL), dict(o=MIS), dict(lse=NULL), dict(dq=NULL), dict(dv=MIS), dict(grad=7), dict(odt=7),
+               dict(ws=NULL), dict(ws=ctypes.c_void_p(0x1000010)), dict(bytes=need - 1), dict(cap=0), dict(block=96),
+               dict(S=200), dict(scale=float("nan")),
+               dict(dq=_at(1)), dict(dk=_at(6)), dict(dv=_at(0)), dict(ws=_at(5)), dict(dk=_at(10)),
+               dict(o_lo=_at(6)), dict(o_lo=_at(12), odt=vsa.F32)):
+        assert call(**kw) == vsa.ERR_INVALID_ARGUMENT, kw
+    assert call(D=96) == vsa.ERR_UNSUPPORTED
+
+
+def test_tiled_backward_argument_errors(L):
+    def call(grid=(2, 8, 16), tiles=((1, 8, 16),), stride=0, bytes=1 << 22):
+        arr, n = _tiles(*tiles)
+        return L.vsa_block_sparse_attention_tiled_backward(
+            _at(0), _at(1), _at(2), _at(3), _at(4), vsa.BF16, NULL, _at(5), _at(6), _at(7), _at(8), vsa.BF16, 1, 2,
+            256, 64, Dims3(*grid), arr, n, NULL, _at(10), _at(11), 2, 1, stride, 0.0, _at(9), bytes, NULL)
+    assert call(grid=(2, 8, 8)) == vsa.ERR_INVALID_ARGUMENT
+    assert call(tiles=((1, 8, 16), (2, 8, 16))) == vsa.ERR_INVALID_ARGUMENT
+    assert call(tiles=((1, 3, 16),)) == vsa.ERR_INVALID_ARGUMENT
+    assert call(stride=3) == vsa.ERR_INVALID_ARGUMENT
+    assert call(tiles=((1, 8, 8),), stride=4) == vsa.ERR_UNSUPPORTED
+    assert call(tiles=((4, 4, 8),)) == vsa.ERR_UNSUPPORTED       # the box is larger than the grid
+    assert call(bytes=256) == vsa.ERR_INVALID_ARGUMENT
+
+
+def test_window_bias_argument_errors(L):
+    need = L.vsa_window_attention_lse_workspace_size(2, 256, 32, 128)
+    assert need >= 2 * 32 * 4 + 257
+    assert L.vsa_window_attention_lse_workspace_size(2, 256, 0, 128) == 0     # no bias
+    bad = [(3, 128), (2, 128), (258, 500), (31, 128), (32, 8), (32, 0), (32, (1 << 24) + 1)]
+    for buckets, far in bad:
+        assert L.vsa_window_attention_lse_workspace_size(2, 256, buckets, far) == 0
+
+    def fwd(**kw):
+        a = dict(lse=_at(4), o_lo=NULL, bias=_at(5), bdt=vsa.F32, buckets=32, far=128, ws=_at(9), bytes=need, window=64,
+                 sink=3)
+        a.update(kw)
+        return L.vsa_window_attention_lse(_at(0), _at(1), _at(2), _at(3), vsa.BF16, a["lse"], a["o_lo"], 1, 2, 256, 64,
+                                          a["window"], a["sink"], 0.0, a["bias"], a["bdt"], a["buckets"], a["far"],
+                                          a["ws"], a["bytes"], NULL)
+    need_b = L.vsa_window_attention_backward_workspace_size(1, 2, 256, 32, 128)
+    assert need_b > L.vsa_window_attention_backward_workspace_size(1, 2, 256, 0, 0) > 0
+
+    def bwd(**kw):
+        a = dict(bias=_at(10), bdt=vsa.F32, buckets=32, far=128, dbias=_at(11), ws=_at(9), bytes=need_b, window=64, sink=3)
+        a.update(kw)
+        return L.vsa_window_attention_backward(_at(0), _at(1), _at(2), _at(3), _at(4), vsa.BF16, NULL, _at(5), _at(6),
+                                               _at(7), _at(8), vsa.BF16, 1, 2, 256, 64, a["window"], a["sink"], 0.0,
+                                               a["bias"], a["bdt"], a["buckets"], a["far"], a["dbias"], a["ws"],
+                                               a["bytes"], NULL)
+    for call in (fwd, bwd):
+        for buckets, far in bad:
+            assert call(buckets=buckets, far=far) == vsa.ERR_INVALID_ARGUMENT
+        for kw in (dict(bdt=5), dict(bias=ctypes.c_void_p(0x1002)), dict(bytes=0), dict(ws=NULL), dict(window=0),
+                   dict(sink=257), dict(sink=-1), dict(ws=_at(1))):
+            assert call(**kw) == vsa.ERR_INVALID_ARGUMENT, kw
+    assert bwd(bias=NULL) == vsa.ERR_INVALID_ARGUMENT and "needs a bias" in vsa.last_error()
+    assert bwd(dbias=_at(6)) == vsa.ERR_INVALID_ARGUMENT
+    assert L.vsa_relative_position_buckets(32, 8, _at(0), NULL) == vsa.ERR_INVALID_ARGUMENT
+    assert L.vsa_relative_position_buckets(32, 128, NULL, NULL) == vsa.ERR_INVALID_ARGUMENT
+
+
+def test_transpose_block_lists_argument_errors(L):
+    assert L.vsa_transpose_block_lists_workspace_size(2, 100) == 0
+    need = L.vsa_transpose_block_lists_workspace_size(2, 300)
+    assert need == 2 * 10 * 300 * 4 + (-(2 * 10 * 300 * 4) % 256)
+
+    def call(**kw):
+        a = dict(idx=_at(0), cnt=_at(1), lists=2, nb=300, cap=4, off=_at(2), rows=_at(3), ws=_at(4), bytes=need)
+        a.update(kw)
+        return L.vsa_transpose_block_lists(a["idx"], a["cnt"], a["lists"], a["nb"], a["cap"], a["off"], a["rows"],
+                                           a["ws"], a["bytes"], NULL)
+    for kw in (dict(idx=NULL), dict(cnt=NULL), dict(off=NULL), dict(rows=NULL), dict(lists=0), dict(lists=65536),
+               dict(nb=0), dict(cap=0), dict(nb=1 << 16, cap=1 << 16), dict(bytes=need - 1), dict(ws=NULL),
+               dict(rows=_at(0)), dict(off=_at(1)), dict(ws=_at(3))):
+        assert call(**kw) == vsa.ERR_INVALID_ARGUMENT, kw
