@@ -489,9 +489,9 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                         for (int u = 0; u < BN / 32; ++u) {
                             // a bucket border crosses a few of the tile's 32 x 32 pieces only
                             const BiasPiece piece = bias_piece(bk[u], bk[u + 1]);
-                            const float hi = sTab[piece.hi];
-                            if (piece.uniform) {
-                                const uint64_t sx = f32x2(a.scale_log2, a.scale_log2), bx = f32x2(hi, hi);
+                            if (piece.kind == BIAS_ONE) {
+                                const float b = sTab[piece.first];
+                                const uint64_t sx = f32x2(a.scale_log2, a.scale_log2), bx = f32x2(b, b);
                                 #pragma unroll
                                 for (int i = 32 * u; i < 32 * u + 32; i += 2) {
                                     float y0, y1;
@@ -500,8 +500,15 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                                     x[i] = __float_as_uint(y0);
                                     x[i + 1] = __float_as_uint(y1);
                                 }
+                            } else if (piece.kind == BIAS_TWO) {
+                                const float b0 = sTab[piece.first], b1 = sTab[piece.second];
+                                const uint32_t second = bias_second(piece, lane);
+                                #pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    x[32 * u + i] = __float_as_uint(fmaf(__uint_as_float(x[32 * u + i]), a.scale_log2,
+                                                                         (second >> i) & 1u ? b1 : b0));
                             } else {
-                                const float lo = sTab[piece.lo];
+                                const float lo = sTab[piece.lo], hi = sTab[piece.hi];
                                 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     x[32 * u + i] = __float_as_uint(fmaf(__uint_as_float(x[32 * u + i]), a.scale_log2,

@@ -363,7 +363,7 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                     #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         piece[u] = bias_piece(bk[u], bk[u + 1]);
-                        if (piece[u].uniform) flat[u] = sTab[piece[u].hi];
+                        if (piece[u].kind == BIAS_ONE) flat[u] = sTab[piece[u].first];
                     }
                 }
                 tmem_ld_wait();
@@ -382,7 +382,13 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                 if constexpr (BIAS) {
                     #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        if (!piece[u].uniform) {
+                        if (piece[u].kind == BIAS_TWO) {
+                            const float b0 = sTab[piece[u].first], b1 = sTab[piece[u].second];
+                            const uint32_t second = bias_second(piece[u], lane);
+                            #pragma unroll
+                            for (int c = 32 * u; c < 32 * u + 32; ++c)
+                                x[c] = __float_as_uint(__uint_as_float(x[c]) + ((second >> (c & 31)) & 1u ? b1 : b0));
+                        } else if (piece[u].kind == BIAS_MORE) {
                             const float lo = sTab[piece[u].lo], hi = sTab[piece[u].hi];
                             #pragma unroll
                             for (int c = 32 * u; c < 32 * u + 32; ++c)
@@ -453,10 +459,10 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (!a.dbias_part) break;
-                    if (piece[u].uniform) {
-                        if (piece[u].hi != run_bucket[u]) {
+                    if (piece[u].kind == BIAS_ONE) {
+                        if (piece[u].first != run_bucket[u]) {
                             flush(u);
-                            run_bucket[u] = piece[u].hi;
+                            run_bucket[u] = piece[u].first;
                         }
                         uint64_t t0 = 0, t1 = 0;  // two pairs of fp32 zeros
                         #pragma unroll
@@ -467,6 +473,24 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
                         float a0, a1;
                         f32x2_split(add_f32x2(t0, t1), a0, a1);
                         run_sum[u] += a0 + a1;
+                    } else if (piece[u].kind == BIAS_TWO) {
+                        const uint32_t second = bias_second(piece[u], lane);
+                        float t0 = 0.f, t1 = 0.f;
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if ((second >> i) & 1u) t1 += pr[32 * u + i];
+                            else t0 += pr[32 * u + i];
+                        }
+                        #pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) {
+                            t0 += __shfl_xor_sync(0xffffffffu, t0, o);
+                            t1 += __shfl_xor_sync(0xffffffffu, t1, o);
+                        }
+                        if (lane == 0) {
+                            part[piece[u].first] += t0;
+                            part[piece[u].second] += t1;
+                        }
+                        __syncwarp();
                     } else {
                         // sums of the piece's diagonals: element (r, i) goes to lane (i - r) mod 32
                         float diag[2] = {0.f, 0.f};  // i - r = lane - 32 and lane

@@ -1,11 +1,15 @@
 // relative_bias.cuh -- a relative position bias inside an attention tile.
 //
-// The bias of a 32 x 32 piece of a tile depends on j - i alone: 63 offsets.
+// The bias of a 32 x 32 piece of a tile depends on j - i alone: 63 diagonals.
 // Lane l of the warp that holds the piece's 32 rows keeps the buckets of two of
-// them, (first diagonal - 32 + l) and (first diagonal + l); element (row lane r,
-// column i) is on diagonal i - r, whose value is in lane (i - r) mod 32 and
-// takes one shuffle.  Buckets widen with distance, so most pieces have a single
-// bucket and one value for all 1024 elements.
+// them, l - 32 and l (element (row lane r, column i) is on diagonal i - r).
+// Buckets widen with distance, so a piece is one of three kinds:
+//   one bucket: one value for all 1024 elements;
+//   two, with one border: columns below r + border take the first value;
+//   more (close to the main diagonal): diagonal m's value is in lane m mod 32
+//   and takes one shuffle per element.
+// Shuffles have an eighth of the rate of a select, so the second kind, which is
+// half of all pieces where 64 buckets reach 2048 positions, has its own path.
 //
 // The bucket of every offset is one byte in global memory (relative_bias.cu);
 // a tile's bytes are asked for one tile ahead, while the warp would wait for
@@ -14,6 +18,8 @@
 #pragma once
 
 #include <stdint.h>
+
+#include "common.cuh"
 
 namespace vsa {
 
@@ -24,14 +30,28 @@ __device__ __forceinline__ int bias_bucket(const uint8_t *bm, int R, int o) {
     return __ldg(bm + min(max(o, -R), R));
 }
 
+enum : int { BIAS_ONE = 0, BIAS_TWO = 1, BIAS_MORE = 2 };
 struct BiasPiece {
-    int lo, hi;      // this lane's two buckets
-    bool uniform;    // one bucket for the whole piece: hi, in every lane
+    int lo, hi;         // this lane's two buckets
+    int kind;           // the rest is the same in every lane
+    int first, second;  // buckets of the first and the last diagonal
+    int border;         // BIAS_TWO: the first diagonal of `second`
 };
 __device__ __forceinline__ BiasPiece bias_piece(int lo, int hi) {
-    const int b0 = __shfl_sync(0xffffffffu, hi, 0);
-    return BiasPiece{lo, hi, __all_sync(0xffffffffu, lo == b0 && hi == b0) != 0};
+    BiasPiece p{lo, hi, BIAS_MORE, __shfl_sync(0xffffffffu, lo, 1), __shfl_sync(0xffffffffu, hi, 31), 0};
+    // lane 0's diagonal -32 is outside the piece
+    const uint32_t a0 = __ballot_sync(0xffffffffu, lo == p.first) | 1u, a1 = __ballot_sync(0xffffffffu, hi == p.first);
+    const uint32_t b0 = __ballot_sync(0xffffffffu, lo == p.second) & ~1u, b1 = __ballot_sync(0xffffffffu, hi == p.second);
+    const uint64_t a = static_cast<uint64_t>(a1) << 32 | a0, b = static_cast<uint64_t>(b1) << 32 | b0;
+    if (a == ~0ull) p.kind = BIAS_ONE;
+    else if (a == ~b && (a & (a + 1)) == 0) {
+        p.kind = BIAS_TWO;
+        p.border = __popcll(a) - 32;
+    }
+    return p;
 }
+// BIAS_TWO: the row's columns that take the second value, as bits.
+__device__ __forceinline__ uint32_t bias_second(const BiasPiece &p, int lane) { return span_bits(0, lane + p.border, 32); }
 // Element (row lane, column i)'s value from the values of this lane's buckets.
 __device__ __forceinline__ float bias_at(float lo, float hi, int i, int lane) {
     return __shfl_sync(0xffffffffu, lane <= i ? hi : lo, (i - lane) & 31);
