@@ -352,13 +352,9 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
                 if constexpr (BIAS) {
                     #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        if (piece[u].kind == BIAS_TWO) {
-                            const float b0 = sTab[piece[u].first], b1 = sTab[piece[u].second];
-                            const uint32_t second = bias_second(piece[u], lane);
-                            #pragma unroll
-                            for (int c = 32 * u; c < 32 * u + 32; ++c)
-                                x[c] = __float_as_uint(__uint_as_float(x[c]) + ((second >> (c & 31)) & 1u ? b1 : b0));
-                        } else if (piece[u].kind == BIAS_MORE) {
+                        // shuffles for both other kinds: here a path of selects for one border
+                        // measured 2.25 ms against 2.17 (S = 30720, 24 heads, 64 buckets to 2048)
+                        if (piece[u].kind != BIAS_ONE) {
                             const float lo = sTab[piece[u].lo], hi = sTab[piece[u].hi];
                             #pragma unroll
                             for (int c = 32 * u; c < 32 * u + 32; ++c)
