@@ -641,6 +641,114 @@ def test_bias_without_its_gradient():
     assert torch.equal(torch.autograd.grad(o, leaf, g)[0], want[0])
 
 
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.float32).min])
+def test_bias_that_masks(low):
+    """A table entry of the type's lowest value, or -inf, takes its bucket out; a row left without keys is empty."""
+    S, D, H, far = 300, 64, 2, 64
+    q, k, v, g = inputs(1, H, S, D, seed=31)
+    bias = torch.randn(16, H, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    bias[8:, 0] = low    # head 0: no later key
+    bias[3, 1] = low     # head 1: one bucket among others (distance 3 backwards)
+    bias[0, 1] = bias[1, 1] = 2.0
+    f = [bucket_of(d, 16, far) for d in range(far + 1)]
+    i = torch.arange(S, device=DEV)
+    r = i[None, :] - i[:, None]
+    bucket = torch.tensor(f, device=DEV)[r.abs().clamp(max=far)] + (r > 0) * 8
+    o, lse, o_lo = vsa.window_attention(q, k, v, 120, 2, bias=bias, max_distance=far, return_remainder=True)
+    *grads, dbias = vsa.window_attention_backward(g, q, k, v, o, lse, 120, 2, bias=bias, max_distance=far,
+                                                  grad_dtype=torch.float32, o_lo=o_lo)
+    vsa.device_status()
+    want, err = (torch.zeros(16, H, dtype=torch.float64, device=DEV) for _ in range(2))
+    for h in range(H):
+        b = bias[:, h].double()
+        see = window_mask(S, 120, 2) & (b > -1e30)[bucket]
+        ref = reference(q[0, h], k[0, h], v[0, h], g[0, h], see, None, b.clamp(min=-1e30)[bucket])
+        check([x[0, h] for x in grads], ref, what=f"head {h}")
+        want[:, h].index_add_(0, bucket.view(-1), ref["dX"].view(-1))
+        err[:, h].index_add_(0, bucket.view(-1), ref["e_dX"].view(-1))
+    assert ((dbias.double() - want).abs() <= err + 1e-6).all()
+    assert not dbias[8:, 0].any() and dbias[3, 1] == 0
+    # every bucket taken out: every row is empty, nothing is passed on
+    bias.fill_(low)
+    o, lse = vsa.window_attention(q, k, v, 120, 2, bias=bias, max_distance=far, return_lse=True)
+    with pytest.raises(RuntimeError):
+        vsa.device_status()
+    assert not o.any() and (lse == -math.inf).all()
+    out = vsa.window_attention_backward(g, q, k, v, o, lse, 120, 2, bias=bias, max_distance=far)
+    assert not any(x.any() for x in out)
+
+
+def test_non_finite_rows_stay_with_their_neighbours():
+    """A NaN in one query's gradient reaches that query, the keys it sees and no other head or block."""
+    D, block, nb = 64, 128, 4
+    q, k, v, g = inputs(1, 2, nb * block, D, seed=32)
+    idx = torch.tensor([[0], [0], [2], [3]], dtype=torch.int32, device=DEV)
+    cnt = torch.ones(nb, dtype=torch.int32, device=DEV)
+    o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, block, return_lse=True)
+    clean = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block)
+    g[0, 0, 130, 5] = math.nan
+    dq, dk, dv = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block)
+    assert dq[0, 0, 130].isnan().any()
+    for x, y in zip((dq, dk, dv), clean):
+        assert torch.equal(x[0, 1], y[0, 1]) and torch.equal(x[0, 0, 2 * block:], y[0, 0, 2 * block:])
+    assert torch.equal(dq[0, 0, :block], clean[0][0, 0, :block])
+    other = torch.arange(block, 2 * block, device=DEV) != 130
+    assert torch.equal(dq[0, 0, block:2 * block][other], clean[0][0, 0, block:2 * block][other])
+
+
+@pytest.mark.parametrize("block,nb,longest", [(32, 260, 30), (128, 140, 9)])
+def test_backward_over_many_blocks(block, nb, longest):
+    """More than 128 blocks: the lists are turned in global memory.  Sampled against the dense formula."""
+    D, S = 64, block * nb
+    q, k, v, g = inputs(1, 1, S, D, seed=nb)
+    idx, cnt = random_lists(1, 1, nb, longest, seed=nb)
+    idx[..., 0] = 0  # one block that every query block lists, as a sink is
+    o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, block, return_lse=True)
+    got = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block, grad_dtype=torch.float32)
+    see = list_mask(idx[0, 0], cnt[0, 0], block, S)
+    check([x[0, 0] for x in got], reference(q[0, 0], k[0, 0], v[0, 0], g[0, 0], see))
+
+
+def test_two_streams_at_once():
+    q, k, v, g = inputs(1, 2, 1024, 64, seed=33)
+    idx, cnt = random_lists(1, 2, 8, 5, seed=33)
+    o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, 128, return_lse=True)
+    want = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, 128)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = []
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                out.append(vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, 128))
+    torch.cuda.synchronize()
+    for res in out:
+        for x, y in zip(res, want):
+            assert torch.equal(x, y)
+
+
+def test_mixed_input_types():
+    """An fp32 q beside bf16 k and v: each gradient in its input's type, from the same roundings."""
+    q, k, v, g = inputs(1, 2, 256, 64, seed=34)
+    leaves = [q.float().requires_grad_(), k.clone().requires_grad_(), v.clone().requires_grad_()]
+    o = vsa.window_attention(*leaves, 64, 2, out_dtype=torch.bfloat16)
+    got = torch.autograd.grad(o, leaves, g)
+    o2, lse, o_lo = vsa.window_attention(q, k, v, 64, 2, return_remainder=True)
+    want = vsa.window_attention_backward(g, q, k, v, o2, lse, 64, 2, o_lo=o_lo, grad_dtype=torch.float32)
+    assert torch.equal(o, o2) and [x.dtype for x in got] == [torch.float32, torch.bfloat16, torch.bfloat16]
+    for x, y in zip(got, want):
+        assert torch.equal(x, y.to(x.dtype))
+
+
+def test_backward_of_a_backward_is_refused():
+    q, k, v, g = inputs(1, 1, 128, 64, seed=35)
+    leaf = q.requires_grad_()
+    o = vsa.window_attention(leaf, k, v, 64)
+    (grad,) = torch.autograd.grad(o, leaf, g, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(grad.sum(), leaf)
+
+
 def test_refusals():
     q, k, v, g = inputs(1, 2, 256, 64, seed=15)
     idx, cnt = random_lists(1, 2, 2, 2, seed=15)
