@@ -21,6 +21,27 @@ namespace {
 
 constexpr int kKeysAtOnce = 8192;  // key blocks whose words a CTA holds (32 KB)
 
+// A warp reads and checks one query block's list: its first 128 entries, 32 u +
+// lane in v[u], with all loads in flight at once; false if it is invalid (it
+// then names nothing).
+__device__ __forceinline__ bool list_row(const int32_t *row, int n, int nb, int cap, int lane, int (&v)[4]) {
+    bool ok = n >= 0 && n <= cap;
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = ok && 32 * u + lane < n ? __ldg(row + 32 * u + lane) : -1;
+    int last = -1;  // the entry before this run of 32
+    #pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int up = __shfl_up_sync(0xffffffffu, v[u], 1);
+        if (32 * u + lane < n) ok = ok && v[u] >= 0 && v[u] < nb && (lane == 0 ? last : up) < v[u];
+        last = __shfl_sync(0xffffffffu, v[u], 31);
+    }
+    for (int j = 128 + lane; ok && j < n; j += 32) {
+        const int x = __ldg(row + j);
+        ok = x >= 0 && x < nb && __ldg(row + j - 1) < x;
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // One CTA per (32 query blocks, list).
 __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t *__restrict__ idx, const int32_t *__restrict__ cnt,
                                                         int nb, int cap, uint32_t *__restrict__ bits, int *status) {
@@ -37,19 +58,19 @@ __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t *__restric
             if (q >= nb) break;
             const int n = __ldg(cnt + list * nb + q);
             const int32_t *row = idx + (list * nb + q) * cap;
-            bool ok = n >= 0 && n <= cap;
-            for (int j = lane; ok && j < n; j += 32) {
-                const int v = __ldg(row + j);
-                ok = v >= 0 && v < nb && (j == 0 || __ldg(row + j - 1) < v);
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {  // an invalid list names nothing
+            int v[4];
+            if (!list_row(row, n, nb, cap, lane, v)) {
                 if (lane == 0 && k0 == 0) report(status, DEV_RUNTIME);
                 continue;
             }
-            for (int j = lane; j < n; j += 32) {
-                const int v = __ldg(row + j) - k0;
-                if (v >= 0 && v < keys) atomicOr(&word[v], 1u << r);
+            #pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int x = v[u] - k0;
+                if (32 * u + lane < n && x >= 0 && x < keys) atomicOr(&word[x], 1u << r);
+            }
+            for (int j = 128 + lane; j < n; j += 32) {
+                const int x = __ldg(row + j) - k0;
+                if (x >= 0 && x < keys) atomicOr(&word[x], 1u << r);
             }
         }
         __syncthreads();
@@ -150,22 +171,8 @@ __global__ void __launch_bounds__(1024) list_turn_kernel(const int32_t *__restri
     for (int q = warp; q < nb; q += 32) {
         const int n = __ldg(cnt + list * nb + q);
         const int32_t *row = idx + (list * nb + q) * cap;
-        bool ok = n >= 0 && n <= cap;
         int v[4];
-        #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = ok && 32 * u + lane < n ? __ldg(row + 32 * u + lane) : -1;
-        int last = -1;  // the entry before this run of 32
-        #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int up = __shfl_up_sync(0xffffffffu, v[u], 1);
-            if (32 * u + lane < n) ok = ok && v[u] >= 0 && v[u] < nb && (lane == 0 ? last : up) < v[u];
-            last = __shfl_sync(0xffffffffu, v[u], 31);
-        }
-        for (int j = 128 + lane; ok && j < n; j += 32) {
-            const int x = __ldg(row + j);
-            ok = x >= 0 && x < nb && __ldg(row + j - 1) < x;
-        }
-        if (!__all_sync(0xffffffffu, ok)) {  // an invalid list names nothing
+        if (!list_row(row, n, nb, cap, lane, v)) {
             if (lane == 0) report(status, DEV_RUNTIME);
             continue;
         }
