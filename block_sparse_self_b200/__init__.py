@@ -584,7 +584,9 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     (fp32 [B, H, S]), which block_sparse_attention_backward takes, and
     return_remainder=True what rounding the output to bf16 left as well
     (o, lse, o_lo; None for an fp32 output): with it the backward pass is as
-    exact as with an fp32 output.
+    exact as with an fp32 output.  With either, and where gradients are
+    recorded, blocks of 32 and 64 tokens run on a kernel of their own whose
+    output is rounded differently.
     Differentiable in q, k and v; the lists are constants of the backward pass."""
     if _wants_grad(q, k, v):
         o, lse, o_lo = _BlockSparse.apply(q, k, v, block_sparse_attention, block_sparse_attention_backward,

@@ -46,8 +46,6 @@ struct AttnArgs {
     float scale_log2;
     void *out;
     int out_f32;
-    float *lse;  // optional per-row log-sum-exp, see AttnLaunch
-    void *o_lo;  // optional remainder of a bf16 o, see AttnLaunch
     int *status;
     // tiled mode
     int H, W;  // the padded grid's frame
@@ -507,15 +505,11 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
                                                 pack_bf16x2(__uint_as_float(u[4]) * inv, __uint_as_float(u[5]) * inv),
                                                 pack_bf16x2(__uint_as_float(u[6]) * inv, __uint_as_float(u[7]) * inv));
                         }
-                        if (a.o_lo) store_remainder(o, inv, static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D + 32 * c);
                     }
                 }
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);  // empty key set
-            if (a.lse && row_valid)
-                a.lse[orow] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : l_sum == 0.f ? -INFINITY : l_sum;
         } else if (row_valid && !list_valid) {
-            if (a.lse) a.lse[orow] = -INFINITY;
             // invalid list: the row is written as zeros
             if (a.out_f32) {
                 float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
@@ -523,10 +517,6 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const AttnArgs a) {
             } else {
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D);
                 for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (a.o_lo) {
-                    uint4 *lo = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o_lo) + orow * D);
-                    for (int e = 0; e < D / 8; ++e) lo[e] = make_uint4(0u, 0u, 0u, 0u);
-                }
             }
         }
     }
@@ -579,8 +569,6 @@ vsa_status run(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.out = L.o;
     a.out_f32 = L.out_f32;
-    a.lse = L.lse;
-    a.o_lo = L.o_lo;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;
@@ -672,7 +660,8 @@ bool make_box_map(CUtensorMap *m, const void *ptr, int D, int T, int H, int W, i
 }
 
 vsa_status launch_attention(const AttnLaunch &L, int *status, cudaStream_t st) {
-    if (L.block == 128) return launch_attention_pp(L, status, st);  // two query tiles per CTA
+    // two query tiles per CTA; also the forward passes that keep lse, whatever the block
+    if (L.block == 128 || L.lse) return launch_attention_pp(L, status, st);
     if (L.tiled) {
         const bool pad = L.Tp * L.Hp * L.Wp != L.S;
         if (L.D == 128) {

@@ -115,7 +115,8 @@ constexpr float kMaxRowSum = 16777216.0f;
 
 struct TileSched {
     int qt;       // query tile index, -1 if this CTA has no such tile
-    int n;        // key blocks
+    int n;        // key blocks (key tiles once the list is checked: several short blocks make one)
+    int count;    // blocks of 32 or 64: key blocks
     int r0_len, r1_start;
     const int32_t *list;
 };
@@ -171,11 +172,22 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // BIAS (window mode only): a relative position bias is added to the logits,
 // one value per tile where its offsets share a bucket, else by shuffles (see
 // relative_bias.cuh).
-template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false>
+//
+// BS (lists only): tokens per block.  128, or 32 and 64 for the forward passes
+// that keep lse: a query tile is then one block in the first BS rows of its MMA
+// tile (the warps past them only keep the barriers' phases), and 128 / BS listed
+// key blocks fill a key tile's 128 columns, so that QK^T and PV run at full width
+// and two query tiles alternate.  Against attention.cu's kernel, one block per
+// step and one query block per CTA: 1.04 ms against 1.85 at D = 128 (16 x 45 x 80
+// grid, 4 heads, 64-token tiles, 62 blocks listed), the same 89 us at D = 64 (2 x 5
+// heads of 120 blocks, 14 listed).  The columns past a list's end repeat its last
+// block, masked.
+template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false, int BS = 128>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     using C = PPCfg<D>;
-    constexpr int BN = 128;
+    constexpr int BN = 128, NSUB = BN / BS;
+    static_assert(BS == 128 || !WINDOW, "windows run on 128-token tiles");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = base;                                  // [2][TILE]
@@ -280,14 +292,24 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             }
         }
     }
+    if constexpr (BS < 128) {
+        for (int t = 0; t < 2; ++t) {
+            ts[t].count = ts[t].n;
+            ts[t].n = (ts[t].n + NSUB - 1) / NSUB;
+        }
+    }
+    // listed block of column c of key tile j
+    auto block_at = [&](const TileSched &t, int j, int c) -> int {
+        return __ldg(t.list + min(j * NSUB + c / BS, t.count - 1));
+    };
     const CUtensorMap *tmQ = &maps.q[tc], *tmK = &maps.k[tc], *tmV = &maps.v[tc];
-    // one 128-row tile of Q, K or V: block b of this head
+    // one block of Q, K or V: block b of this head
     auto load_tile = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int b) {
         if constexpr (TILED) {
             const BoxCoord c = box_of(static_cast<uint32_t>(b), a.geom[tc], th, tw);
             for (int s = 0; s < C::KSLABS; ++s) tma_load_5d(dst + s * C::SLAB, map, bar, s * 64, c.w, c.h, c.t, bh);
         } else {
-            for (int s = 0; s < C::KSLABS; ++s) tma_load_3d(dst + s * C::SLAB, map, bar, s * 64, b * BN, bh);
+            for (int s = 0; s < C::KSLABS; ++s) tma_load_3d(dst + s * C::SLAB, map, bar, s * 64, b * BS, bh);
         }
     };
     const int nA = ts[0].n, nB = ts[1].n;
@@ -301,7 +323,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             tma_prefetch_desc(tmK);
             tma_prefetch_desc(tmV);
             const int nq_loaded = (nA > 0) + (nB > 0);
-            mbar_arrive_expect_tx(q_full, nq_loaded * C::TILE_BYTES);
+            mbar_arrive_expect_tx(q_full, nq_loaded * (C::TILE_BYTES / NSUB));
             for (int t = 0; t < 2; ++t)
                 if (ts[t].n > 0) load_tile(sQ + t * C::TILE_BYTES, tmQ, q_full, ts[t].qt);
             uint32_t kc = 0, vc = 0;
@@ -315,9 +337,14 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 if (c >= static_cast<uint32_t>(depth) && !mbar_wait(empty, ((c / depth) - 1) & 1, abort_flag))
                     return false;
                 uint8_t *dst = (is_k ? sK : sV) + slot * C::TILE_BYTES;
-                const int kb = kblock_of<WINDOW>(ts[t], j);
                 mbar_arrive_expect_tx(full, C::TILE_BYTES);
-                load_tile(dst, is_k ? tmK : tmV, full, kb);
+                if constexpr (BS == 128) {
+                    load_tile(dst, is_k ? tmK : tmV, full, kblock_of<WINDOW>(ts[t], j));
+                } else {
+                    #pragma unroll
+                    for (int u = 0; u < NSUB; ++u)
+                        load_tile(dst + u * BS * 128, is_k ? tmK : tmV, full, block_at(ts[t], j, u * BS));
+                }
                 ++c;
                 return true;
             };
@@ -412,9 +439,9 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         const int row = wq * 32 + lane;           // row of the tile
         const TileSched &sc = ts[t];
         const int n = sc.n;
-        const int q0 = (sc.qt < 0 ? 0 : sc.qt) * BN;
+        const int q0 = (sc.qt < 0 ? 0 : sc.qt) * BS;
         const int rg = q0 + row;
-        bool row_valid = sc.qt >= 0 && rg < S;
+        bool row_valid = sc.qt >= 0 && row < BS && rg < S;
         // output row: the permuted position itself, or its T-major token in tiled mode
         uint32_t orow_in_head = rg;
         if constexpr (PAD) {
@@ -442,18 +469,55 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
+            // padded grid: which of the key block's 128 columns are real tokens
+            // (column u * 32 + lane in bit lane of kv[u]); all ones off the edge
+            uint32_t kv[4] = {~0u, ~0u, ~0u, ~0u};
+            bool key_edge = false;
+            if constexpr (BS < 128) {
+                // columns of other groups, in the padding, past the list's end
+                if (a.group > 0) {
+                    const int g0 = (rg / a.group) * a.group;
+                    #pragma unroll
+                    for (int u = 0; u < 4; ++u) kv[u] = span_bits(block_at(sc, j, 32 * u) * BS + (32 * u) % BS, g0, g0 + a.group);
+                    key_edge = true;
+                }
+                if constexpr (PAD) {
+                    #pragma unroll 1
+                    for (int u = 0; u < 4; ++u) {
+                        const PPArgs::BoxGeom &g = a.geom[tc];
+                        const BoxCoord c = box_of(static_cast<uint32_t>(block_at(sc, j, 32 * u)), g, th, tw);
+                        if (c.t + g.bt <= a.real.T && c.h + th <= a.real.H && c.w + tw <= a.real.W) continue;
+                        const uint32_t col = static_cast<uint32_t>((32 * u) % BS + lane);
+                        const uint32_t dt = fdiv(col, g.bhw), r2 = col - dt * g.bhw.d;
+                        const uint32_t dh = fdiv(r2, g.bw), dw = r2 - dh * g.bw.d;
+                        const uint32_t real = __ballot_sync(0xffffffffu, c.t + static_cast<int>(dt) < a.real.T &&
+                                                                             c.h + static_cast<int>(dh) < a.real.H &&
+                                                                             c.w + static_cast<int>(dw) < a.real.W);
+                        key_edge = true;
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e == u) kv[e] &= real;
+                    }
+                }
+                if ((j + 1) * NSUB > sc.count) {
+                    key_edge = true;
+                    #pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (j * NSUB + (32 * u) / BS >= sc.count) kv[u] = 0u;
+                }
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag))) { ok = false; break; }
+            if (BS < 128 && wq * 32 >= BS) {  // rows past the block
+                if (lane == 0) mbar_arrive(&p_full[t]);
+                continue;
+            }
             tc_fence_after();
             uint32_t x[BN];
             #pragma unroll
             for (int c = 0; c < BN / 32; ++c)
                 tmem_ld32(t_lane + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&x[32 * c]));
             tmem_ld_wait();
-            // padded grid: which of the key block's 128 columns are real tokens
-            // (column u * 32 + lane in bit lane of kv[u]); all ones off the edge
-            uint32_t kv[4] = {~0u, ~0u, ~0u, ~0u};
-            bool key_edge = false;
-            if constexpr (PAD) {
+            if constexpr (BS == 128 && PAD) {
                 {
                     const PPArgs::BoxGeom &g = a.geom[tc];
                     const BoxCoord c = box_of(static_cast<uint32_t>(kblock_of<WINDOW>(sc, j)), g, th, tw);
@@ -540,7 +604,8 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                         }
                     }
                 } else {
-                    if (a.group > 0) {
+                    if (BS < 128) {
+                    } else if (a.group > 0) {
                         const int ks = kblock_of<WINDOW>(sc, j) * BN;
                         // key ks + c is in the row's group iff it lies in [g0, g0 + group)
                         const int g0 = (rg / a.group) * a.group - ks;
@@ -717,14 +782,14 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     }
 }
 
-template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false>
+template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false, int BS = 128>
 vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     using C = PPCfg<D>;
     MapSet maps = {};  // copied into the launch parameters
     bool ok = true;
     if constexpr (TILED) {
         for (int c = 0; c < L.tiles.n; ++c) {
-            const int m = L.tiles.t[c] * L.tiles.h[c] * L.tiles.w[c] / 128;
+            const int m = L.tiles.t[c] * L.tiles.h[c] * L.tiles.w[c] / BS;
             const int bt = L.tiles.t[c] / m, bhh = L.tiles.h[c], bw = L.tiles.w[c];
             // the real tensors: boxes reaching past them read zeros
             ok = ok && make_box_map(&maps.q[c], L.q, D, L.T, L.Hg, L.Wg, L.BH, bt, bhh, bw) &&
@@ -732,11 +797,11 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
                  make_box_map(&maps.v[c], L.v, D, L.T, L.Hg, L.Wg, L.BH, bt, bhh, bw);
         }
     } else {
-        ok = make_tile_map(&maps.q[0], L.q, D, L.S, L.BH, 128) && make_tile_map(&maps.k[0], L.k, D, L.S, L.BH, 128) &&
-             make_tile_map(&maps.v[0], L.v, D, L.S, L.BH, 128);
+        ok = make_tile_map(&maps.q[0], L.q, D, L.S, L.BH, BS) && make_tile_map(&maps.k[0], L.k, D, L.S, L.BH, BS) &&
+             make_tile_map(&maps.v[0], L.v, D, L.S, L.BH, BS);
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
-    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS>;
+    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS, BS>;
     constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -745,7 +810,7 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     const int positions = TILED ? L.Tp * L.Hp * L.Wp : L.S;
     a.S = positions;
     a.S_out = L.S;
-    a.nq = (positions + 127) / 128;
+    a.nq = (positions + BS - 1) / BS;
     a.items = a.nq * L.BH;
     a.nqdiv = make_fastdiv(static_cast<uint32_t>(a.nq));
     a.idx = L.idx;
@@ -780,7 +845,7 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
         auto &g = a.geom[c];
         if (TILED && c < L.tiles.n) {
             const int tt = L.tiles.t[c], th = L.tiles.h[c], tw = L.tiles.w[c];
-            const int m = tt * th * tw / 128;
+            const int m = tt * th * tw / BS;
             g.m = make_fastdiv(m);
             g.nthw = make_fastdiv((L.Hp / th) * (L.Wp / tw));
             g.ntw = make_fastdiv(L.Wp / tw);
@@ -1283,6 +1348,13 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
     return check_cuda(cudaGetLastError(), "attention launch (one key block)");
 }
 
+template <int D, int BS>
+vsa_status run_short(const AttnLaunch &L, bool pad, int *status, cudaStream_t st) {
+    if (!L.tiled) return run_pp<D, false, false, false, false, BS>(L, status, st);
+    return pad ? run_pp<D, false, true, true, false, BS>(L, status, st)
+               : run_pp<D, false, true, false, false, BS>(L, status, st);
+}
+
 }  // namespace
 
 vsa_status launch_attention_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
@@ -1290,6 +1362,11 @@ vsa_status launch_attention_pp(const AttnLaunch &L, int *status, cudaStream_t st
         return L.D == 128 ? run_pp<128, true, false, false, true>(L, status, st)
                           : run_pp<64, true, false, false, true>(L, status, st);
     if (L.window) return L.D == 128 ? run_pp<128, true, false>(L, status, st) : run_pp<64, true, false>(L, status, st);
+    if (L.block != 128) {  // forward passes that keep lse (launch_attention)
+        const bool pad = L.tiled && L.Tp * L.Hp * L.Wp != L.S;
+        return L.D == 128 ? (L.block == 64 ? run_short<128, 64>(L, pad, status, st) : run_short<128, 32>(L, pad, status, st))
+                          : (L.block == 64 ? run_short<64, 64>(L, pad, status, st) : run_short<64, 32>(L, pad, status, st));
+    }
     if (L.cap == 1) {  // lists of one key block
         if (L.tiled) {
             if (L.Tp * L.Hp * L.Wp != L.S)

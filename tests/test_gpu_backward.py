@@ -195,7 +195,9 @@ def test_block_sparse_backward(block, nb, D, longest, shared, group, scale):
         idx = torch.arange(nb, dtype=torch.int32, device=DEV).view(nb, 1).contiguous()
         cnt = torch.ones(nb, dtype=torch.int32, device=DEV)
     o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, block, group, scale, return_lse=True)
-    assert torch.equal(o, vsa.block_sparse_attention(q, k, v, idx, cnt, block, group, scale))
+    plain = vsa.block_sparse_attention(q, k, v, idx, cnt, block, group, scale)
+    # 32- and 64-token blocks have a forward kernel of their own beside lse: o is then rounded differently
+    assert torch.equal(o, plain) if block == 128 else (o - plain).abs().max() <= 4 * U * v.abs().max()
     args = (idx, cnt, block, group, scale)
     low = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, *args)
     full = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, *args, grad_dtype=torch.float32)
