@@ -951,6 +951,10 @@ def spade_attention(q, k, v, grid, tiles, budget: Optional[float] = None, topk: 
     probabilities softmax(top_p_scale * scores), top_p_scale defaulting to
     1/sqrt(D); budget and topk are then unused.
 
+    Differentiable in q, k and v, the tiling choice and the lists being
+    constants of the backward pass; with compensate=True the result carries no
+    gradient.
+
     tiled=True runs the permutation inside the summaries and attention kernels
     (no permuted copies; blocks of 32, 64 or 128 tokens, see tiled_supported); tiled=False
     runs the explicit permute / unpermute steps; None picks tiled when it is

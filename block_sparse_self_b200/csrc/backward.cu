@@ -117,10 +117,45 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     a.ndelta[out] = -delta;
 }
 
+// kmean[bh][t][d]: the mean of the keys of tile t (of its rows that exist).  One
+// CTA per tile: thread (g, c) sums 8 columns of every (2048 / D)-th row; the rows' sums
+// are joined in a fixed order.  Bandwidth bound: K read once.
+template <int D>
+__global__ void __launch_bounds__(256) tile_means_kernel(const __nv_bfloat16 *__restrict__ k, int S, int nt,
+                                                         float *__restrict__ kmean) {
+    constexpr int CH = D / 8, GROUPS = 256 / CH;
+    __shared__ float part[GROUPS][D + 8];
+    const int t = blockIdx.x, bh = blockIdx.y, c = threadIdx.x % CH, g = threadIdx.x / CH;
+    const int rows = min(128, S - t * 128);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const __nv_bfloat16 *src = k + (static_cast<size_t>(bh) * S + static_cast<size_t>(t) * 128) * D + c * 8;
+    #pragma unroll
+    for (int i = 0; i < 128 / GROUPS; ++i) {
+        const int r = i * GROUPS + g;
+        if (r < rows) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * D));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[2 * e] += __uint_as_float(w[e] << 16);
+                s[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+    }
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) part[g][c * 8 + e] = s[e];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float x = 0.f;
+        for (int y = 0; y < GROUPS; ++y) x += part[y][d];
+        kmean[(static_cast<size_t>(bh) * nt + t) * D + d] = x / rows;
+    }
+}
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t nlse, ndelta, none, valid, t_off, t_rows, bits, part, bias, total;
+    size_t nlse, ndelta, none, valid, kmean, t_off, t_rows, bits, part, bias, total;
 };
 
 Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far) {
@@ -136,6 +171,7 @@ Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, i
     L.ndelta = take(BH * Pw * 4);
     L.none = take(256 * 4);
     L.valid = take(BH * (Pw / 32) * 4);
+    if (lists == 0) L.kmean = take(BH * (Pw / 128) * 128 * 4);  // D <= 128
     if (lists > 0) {
         L.t_off = take(static_cast<size_t>(lists) * (nb + 1) * 4);
         L.t_rows = take(static_cast<size_t>(lists) * nb * cap * 4);
@@ -246,6 +282,16 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
         a.R = bias_reach(L.S, B.far);
         a.buckets = buckets;
         a.dbias_part = B.dbias ? f32_at(lay.part) : nullptr;
+    }
+    if (L.window) {
+        float *kmean = f32_at(lay.kmean);
+        const dim3 tiles(a.nt, L.BH);
+        const auto *k = static_cast<const __nv_bfloat16 *>(L.k);
+        if (L.D == 128) tile_means_kernel<128><<<tiles, 256, 0, st>>>(k, L.S, a.nt, kmean);
+        else tile_means_kernel<64><<<tiles, 256, 0, st>>>(k, L.S, a.nt, kmean);
+        const vsa_status r = check_cuda(cudaGetLastError(), "attention backward launch (tile means)");
+        if (r != VSA_OK) return r;
+        a.kmean = kmean;
     }
     const dim3 grid((a.Pw / 32 + 7) / 8, L.BH);
     if (L.D == 128) {

@@ -698,6 +698,58 @@ def test_non_finite_rows_stay_with_their_neighbours():
     assert torch.equal(dq[0, 0, block:2 * block][other], clean[0][0, 0, block:2 * block][other])
 
 
+def test_window_non_finite_rows_stay_alone():
+    """A NaN query and a NaN gradient row reach their own dq rows and the keys they see, no other row's dq."""
+    S, D = 512, 64
+    q, k, v, g = inputs(1, 2, S, D, seed=36)
+    bias = torch.randn(16, 2, device=DEV)
+    q2, g2 = q.clone(), g.clone()
+    q2[0, 0, 200, 3] = math.nan
+    g2[0, 0, 210, 3] = math.inf
+    out = []
+    for qq, gg in ((q, g), (q2, g2)):
+        o, lse = vsa.window_attention(qq, k, v, 40, bias=bias, max_distance=30, return_lse=True)
+        out.append(vsa.window_attention_backward(gg, qq, k, v, o, lse, 40, bias=bias, max_distance=30))
+    others = torch.ones(S, dtype=torch.bool, device=DEV)
+    others[200] = others[210] = False
+    assert not out[1][0][0, 0, 200].isfinite().all() and not out[1][0][0, 0, 210].isfinite().all()
+    # the clean rows' weights of the tiles' means change with the mass of the two rows: rounding only
+    assert (out[1][0][0, 0][others] - out[0][0][0, 0][others]).abs().max() <= 2 * U * out[0][0][0, 0].abs().max()
+    assert torch.equal(out[1][0][0, 1], out[0][0][0, 1])
+    # the tile of queries 128 .. 255 is computed with keys 0 .. 383, where a masked pair is zero times the NaN
+    far = torch.arange(S, device=DEV) >= 384
+    for x, y in zip(out[1][1:3], out[0][1:3]):
+        assert torch.equal(x[0, 0][far], y[0, 0][far]) and torch.equal(x[0, 1], y[0, 1])
+
+
+@pytest.mark.parametrize("S,window,sink", [(640, 60, 0), (900, 300, 150)])
+def test_window_gradients_of_keys_with_a_large_mean(S, window, sink):
+    """Keys far from zero and close to one another: dq depends on their spread alone.
+
+    The errors of dX multiply k - c, with c the weighted mean of the tiles' mean keys (fp32 sums of P over a
+    quarter of the columns).  With keys m + x, |x| much smaller than |m|, |k_j - c| is at most the largest
+    distance of two keys, so the bound of dq takes that in place of |k_j|; the sum of dX that is taken off
+    carries fp32 rounding of S terms of size |dX| only, times |c|."""
+    D = 64
+    q, k, v, g = inputs(1, 1, S, D, seed=S)
+    k = (k.float() * 0.25 + 8 * torch.randn(1, 1, 1, D, generator=torch.Generator(device=DEV).manual_seed(1),
+                                            device=DEV)).bfloat16()
+    q = (q.float() * 0.1).bfloat16()
+    o, lse, o_lo = vsa.window_attention(q, k, v, window, sink, return_remainder=True)
+    dq = vsa.window_attention_backward(g, q, k, v, o, lse, window, sink, grad_dtype=torch.float32, o_lo=o_lo)[0]
+    see = window_mask(S, window, sink)
+    ref = reference(q[0, 0], k[0, 0], v[0, 0], g[0, 0], see)
+    k64 = k[0, 0].double()
+    spread = (k64.amax(0) - k64.amin(0))[None, :]
+    scale = 1 / math.sqrt(D)
+    bound = scale * (ref["e_dX"].sum(1, keepdim=True) * spread
+                     + S * 2.0 ** -24 * ref["dX"].abs().sum(1, keepdim=True) * k64.abs().amax(0)[None, :])
+    assert ((dq[0, 0].double() - ref["dq"]).abs() <= bound + 1e-5).all()
+    # without it the error would be of the size of the mean times the errors of dX
+    rough = (scale * ref["e_dX"] @ k64.abs()).norm()
+    assert (dq[0, 0].double() - ref["dq"]).norm() <= 0.05 * rough
+
+
 @pytest.mark.parametrize("block,nb,longest", [(32, 260, 30), (128, 140, 9)])
 def test_backward_over_many_blocks(block, nb, longest):
     """More than 128 blocks: the lists are turned in global memory.  Sampled against the dense formula."""
