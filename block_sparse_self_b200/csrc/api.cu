@@ -865,7 +865,7 @@ vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int
     VSA_REQUIRE(lists >= 1 && lists <= 65535, "lists must be in [1, 65535], got %d", lists);
     VSA_REQUIRE(nb >= 1 && nb <= (1 << 26), "nb must be in [1, 2^26], got %d", nb);
     VSA_REQUIRE(cap >= 1, "cap must be >= 1, got %d", cap);
-    VSA_REQUIRE(static_cast<long long>(nb) * cap <= 0x7fffffffLL, "nb * cap must be < 2^31");
+    VSA_REQUIRE(static_cast<long long>(nb) * cap <= 1LL << 30, "nb * cap must be <= 2^30");  // 32-bit strides past the end
     VSA_REQUIRE(aligned4(idx) && aligned4(cnt), "idx and cnt must be non-NULL 4-byte aligned device pointers");
     VSA_REQUIRE(aligned4(offsets) && aligned4(rows), "offsets and rows must be non-NULL 4-byte aligned device pointers");
     const size_t need = vsa_transpose_block_lists_workspace_size(lists, nb);
@@ -893,7 +893,7 @@ static vsa_status backward(const void *g, const void *o, vsa_dtype o_dtype, cons
     VSA_REQUIRE(aligned16(g) && aligned16(o), "dout and o must be non-NULL 16-byte aligned device pointers");
     VSA_REQUIRE(aligned4(lse), "lse must be a non-NULL 4-byte aligned device pointer");
     if (!L.window)
-        VSA_REQUIRE(static_cast<long long>(L.nb) * L.cap <= 0x7fffffffLL, "nb * cap must be < 2^31");
+        VSA_REQUIRE(static_cast<long long>(L.nb) * L.cap <= 1LL << 30, "nb * cap must be <= 2^30");
     VSA_REQUIRE(static_cast<long long>(BH) * ((L.tiled ? L.nb : (L.S + L.block - 1) / L.block)) <= 0x7fffffffLL,
                 "too many blocks for one launch");
     VSA_REQUIRE(o_lo == nullptr || (aligned16(o_lo) && o_dtype == VSA_BF16),

@@ -567,7 +567,7 @@ vsa_status vsa_relative_position_buckets(int num_buckets, int max_distance, int3
  *   workspace DEVICE scratch of the _workspace_size call's bytes, 256-byte
  *             aligned; NULL will do where that is 0 (nb <= 128)
  * A query block whose list breaks these rules appears nowhere and sets
- * VSA_ERR_RUNTIME.  nb * cap < 2^31.                                        */
+ * VSA_ERR_RUNTIME.  nb * cap <= 2^30 (in the backward passes too).          */
 size_t vsa_transpose_block_lists_workspace_size(int lists, int nb);
 vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap,
                                      int32_t *offsets, int32_t *rows, void *workspace, size_t workspace_bytes,

@@ -467,3 +467,15 @@ def test_transpose_block_lists_argument_errors(L):
                dict(nb=0), dict(cap=0), dict(nb=1 << 16, cap=1 << 16), dict(bytes=need - 1), dict(ws=NULL),
                dict(rows=_at(0)), dict(off=_at(1)), dict(ws=_at(3))):
         assert call(**kw) == vsa.ERR_INVALID_ARGUMENT, kw
+
+
+def test_lists_whose_strides_pass_32_bits(L):
+    """Loops over nb * cap entries step up to 1024 past the end in 32 bits: 2^30 entries are the most."""
+    for nb, cap in ((1 << 15, (1 << 15) + 1), (1, (1 << 31) - 1), (46340, 46340)):
+        assert L.vsa_transpose_block_lists(_at(0), _at(1), 1, nb, cap, _at(2), _at(3), _at(4), 1 << 40,
+                                           NULL) == vsa.ERR_INVALID_ARGUMENT
+        assert "2^30" in vsa.last_error()
+    assert L.vsa_block_sparse_attention_backward(
+        _at(0), _at(1), _at(2), _at(3), _at(4), vsa.BF16, NULL, _at(5), _at(6), _at(7), _at(8), vsa.BF16, 1, 2, 256, 64,
+        128, _at(10), _at(11), (1 << 30) - 1, 1, 0, 0.0, _at(9), 1 << 40, NULL) == vsa.ERR_INVALID_ARGUMENT
+    assert "2^30" in vsa.last_error()

@@ -565,6 +565,31 @@ def test_permute_gradients():
     assert torch.equal(torch.autograd.grad(t, z, g)[0], vsa.permute(g, grid, tiles))
 
 
+def test_captured_training_step():
+    """A recorded forward and backward pass as one graph, replayed over new values."""
+    q, k, v, g = inputs(1, 2, 512, 64, seed=21)
+    idx, cnt = random_lists(1, 2, 8, 4, seed=21)
+    table = torch.randn(32, 2, device=DEV)
+    leaves = [x.requires_grad_() for x in (q, k, v, table)]
+
+    def step():
+        o = vsa.block_sparse_attention(*leaves[:3], idx, cnt, 64) + vsa.window_attention(*leaves[:3], 96, bias=leaves[3])
+        return (o.detach(), *torch.autograd.grad(o, leaves, g))
+
+    step()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = step()
+    with torch.no_grad():
+        for x, y in zip((q, k, v, g), inputs(1, 2, 512, 64, seed=22)):
+            x.copy_(y)
+        table.mul_(-1)
+    gr.replay()
+    got = [x.clone() for x in out]
+    for x, y in zip(got, step()):
+        assert torch.equal(x, y)
+
+
 def test_captured_and_on_another_stream():
     q, k, v, g = inputs(1, 2, 700, 64, seed=12)
     bias = torch.randn(32, 2, device=DEV).bfloat16()
