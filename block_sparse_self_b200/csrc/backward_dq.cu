@@ -20,8 +20,8 @@
 //   dQ_i = scale (sum_j dX_ij k_j - (sum_j dX_ij) c),
 // an identity for any c.  c is, per 32 rows, the mean key of every tile weighted
 // with the mass of P in it (from a quarter of the columns).  With it dQ's error
-// against 64 bits falls from 4.1e-3 to 2.6e-3 of its norm (window 4096), from
-// 4.8e-3 to 2.4e-3 (window 159; 1.7e-3 is the rounding to bf16).  Block lists
+// against 64 bits falls from 4.1e-3 to 2.6e-3 of its norm (window 4096, S = 16384), from
+// 4.6e-3 to 2.6e-3 (window 159, S = 2048; 1.7e-3 is the rounding to bf16).  Block lists
 // reach over the whole grid, the tiles' means say little there (2.77e-3 to
 // 2.76e-3), and they go without.
 #include "backward.cuh"
