@@ -879,7 +879,7 @@ vsa_status vsa_transpose_block_lists(const int32_t *idx, const int32_t *cnt, int
                                    !overlaps(workspace, need, offsets, n_off) && !overlaps(workspace, need, rows, n_idx))),
                 "offsets, rows and workspace must not overlap one another, idx or cnt");
     return check_cuda(launch_transpose_lists(idx, cnt, lists, nb, cap, offsets, rows, true, workspace,
-                                             status_or_null(stream), as_stream(stream)),
+                                             status_or_null(stream), false, as_stream(stream)),
                       "transpose_block_lists launch");
 }
 

@@ -34,6 +34,7 @@
 // rescaled and the block redone from S, which is still intact in TMEM.
 #include <math.h>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "relative_bias.cuh"
@@ -210,7 +211,6 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.y;
     const int S = a.S;
-    if constexpr (BIAS) bias_table(sTab, a.bias_tab, bh % a.n_heads, a.buckets, threadIdx.x, kThreads);
     TileSched ts[2] = {make_sched<WINDOW>(a, 2 * blockIdx.x, bh), make_sched<WINDOW>(a, 2 * blockIdx.x + 1, bh)};
 
     if (threadIdx.x == 0) {
@@ -253,6 +253,10 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
+    }
+    if constexpr (BIAS) {
+        grid_wait();  // for the expanded bias
+        bias_table(sTab, a.bias_tab, bh % a.n_heads, a.buckets, threadIdx.x, kThreads);
     }
     tc_fence_before();
     __syncthreads();
@@ -858,6 +862,8 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
         }
     }
     dim3 grid((a.nq + 1) / 2, L.BH);
+    if constexpr (BIAS)  // right behind the kernel that expands the bias (see chain.cuh)
+        return check_cuda(launch_kernel(true, kern, grid, dim3(kThreads), smem, st, maps, a), "attention launch (two tiles)");
     kern<<<grid, kThreads, smem, st>>>(maps, a);
     return check_cuda(cudaGetLastError(), "attention launch (two tiles)");
 }

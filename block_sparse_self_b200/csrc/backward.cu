@@ -30,9 +30,13 @@ template <int D, bool O_F32>
 __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ StatArgs a) {
     constexpr int LPR = D / 8, ROWS = 32 / LPR;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
+    grid_release();
     if (blockIdx.x == 0 && bh == 0) a.none[threadIdx.x] = threadIdx.x < 128 ? -INFINITY : 0.f;
     const int p0 = (blockIdx.x * 8 + warp) * 32;
-    if (p0 >= a.Pw) return;
+    if (p0 >= a.Pw) {
+        grid_wait();
+        return;
+    }
     const int p = p0 + lane;
     int tok = p < a.P ? p : -1;
     if (a.tiled && tok >= 0) {
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     const size_t out = static_cast<size_t>(bh) * a.Pw + p;
     a.nlse[out] = nl;
     a.ndelta[out] = -delta;
+    grid_wait();
 }
 
 // kmean[bh][t][d]: the mean of the keys of tile t (of its rows that exist).  One
@@ -127,6 +132,7 @@ __global__ void __launch_bounds__(256) tile_means_kernel(const __nv_bfloat16 *__
     __shared__ float part[GROUPS][D + 8];
     const int t = blockIdx.x, bh = blockIdx.y, c = threadIdx.x % CH, g = threadIdx.x / CH;
     const int rows = min(128, S - t * 128);
+    grid_release();
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const __nv_bfloat16 *src = k + (static_cast<size_t>(bh) * S + static_cast<size_t>(t) * 128) * D + c * 8;
     #pragma unroll
@@ -150,6 +156,7 @@ __global__ void __launch_bounds__(256) tile_means_kernel(const __nv_bfloat16 *__
         for (int y = 0; y < GROUPS; ++y) x += part[y][d];
         kmean[(static_cast<size_t>(bh) * nt + t) * D + d] = x / rows;
     }
+    grid_wait();
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -274,6 +281,8 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
 
+    // one chain of launches (see chain.cuh): bias values and tile means (windows), row
+    // statistics, transposed lists, dQ, dK and dV, the bias's gradient
     if (buckets > 0) {
         const vsa_status r = check_cuda(launch_bias_expand(B.bias, B.bias_f32, B.H, L.S, buckets, B.far, ws + lay.bias,
                                                            &a.tab, &a.bm, st),
@@ -287,25 +296,21 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
         float *kmean = f32_at(lay.kmean);
         const dim3 tiles(a.nt, L.BH);
         const auto *k = static_cast<const __nv_bfloat16 *>(L.k);
-        if (L.D == 128) tile_means_kernel<128><<<tiles, 256, 0, st>>>(k, L.S, a.nt, kmean);
-        else tile_means_kernel<64><<<tiles, 256, 0, st>>>(k, L.S, a.nt, kmean);
-        const vsa_status r = check_cuda(cudaGetLastError(), "attention backward launch (tile means)");
+        const vsa_status r = check_cuda(launch_kernel(buckets > 0, L.D == 128 ? tile_means_kernel<128> : tile_means_kernel<64>,
+                                                      tiles, dim3(256), 0, st, k, L.S, a.nt, kmean),
+                                        "attention backward launch (tile means)");
         if (r != VSA_OK) return r;
         a.kmean = kmean;
     }
     const dim3 grid((a.Pw / 32 + 7) / 8, L.BH);
-    if (L.D == 128) {
-        if (B.o_f32) row_stats_kernel<128, true><<<grid, 256, 0, st>>>(s);
-        else row_stats_kernel<128, false><<<grid, 256, 0, st>>>(s);
-    } else {
-        if (B.o_f32) row_stats_kernel<64, true><<<grid, 256, 0, st>>>(s);
-        else row_stats_kernel<64, false><<<grid, 256, 0, st>>>(s);
-    }
-    vsa_status r = check_cuda(cudaGetLastError(), "attention backward launch (row statistics)");
+    auto row_stats = L.D == 128 ? (B.o_f32 ? row_stats_kernel<128, true> : row_stats_kernel<128, false>)
+                                : (B.o_f32 ? row_stats_kernel<64, true> : row_stats_kernel<64, false>);
+    vsa_status r = check_cuda(launch_kernel(L.window, row_stats, grid, dim3(256), 0, st, s),
+                              "attention backward launch (row statistics)");
     if (r != VSA_OK) return r;
     if (lists > 0) {
         int32_t *off = reinterpret_cast<int32_t *>(ws + lay.t_off), *rows = reinterpret_cast<int32_t *>(ws + lay.t_rows);
-        r = check_cuda(launch_transpose_lists(L.idx, L.cnt, lists, L.nb, L.cap, off, rows, false, ws + lay.bits, status, st),
+        r = check_cuda(launch_transpose_lists(L.idx, L.cnt, lists, L.nb, L.cap, off, rows, false, ws + lay.bits, status, true, st),
                        "attention backward launch (transposed lists)");
         if (r != VSA_OK) return r;
         a.t_off = off;

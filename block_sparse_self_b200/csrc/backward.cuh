@@ -25,6 +25,7 @@
 
 #include <math.h>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "relative_bias.cuh"
@@ -69,11 +70,20 @@ struct BwdArgs {
     } geom[kMaxTiles];
 };
 
-// Tensor maps of q, k, v and g: slot 0 only, or one per candidate tiling.
-struct BwdMaps {
-    CUtensorMap q[kMaxTiles], k[kMaxTiles], v[kMaxTiles], g[kMaxTiles];
+// Tensor maps of q, k, v and g, one per candidate tiling; a kernel that has no
+// tilings takes one of each (a tenth of the parameters that a launch copies).
+template <int N>
+struct BwdMapsOf {
+    CUtensorMap q[N], k[N], v[N], g[N];
 };
+using BwdMaps = BwdMapsOf<kMaxTiles>;
 static_assert(sizeof(BwdMaps) + sizeof(BwdArgs) <= 32764, "kernel parameters");
+
+template <bool TILED>
+auto bwd_maps(const BwdMaps &m) {
+    if constexpr (TILED) return m;
+    else return BwdMapsOf<1>{{m.q[0]}, {m.k[0]}, {m.v[0]}, {m.g[0]}};
+}
 
 constexpr int kBwdThreads = 320;  // warps 0-7 element-wise work, 8 TMA producer, 9 MMA issuer and TMEM owner
 

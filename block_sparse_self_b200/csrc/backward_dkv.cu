@@ -42,7 +42,7 @@ struct DkvCfg {
 
 template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
+bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, const __grid_constant__ BwdArgs a) {
     using C = DkvCfg<D>;
     constexpr int SLAB = 128 * 128, NSUB = 128 / BS;
     extern __shared__ uint8_t smem_raw[];
@@ -76,6 +76,32 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
             kb = a.lead + (id - first) - bh * per;
         }
     }
+    grid_release();
+    if (threadIdx.x == 0) {
+        mbar_init(kv_full, 1);
+        for (int s = 0; s < C::NQ; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+        }
+        for (int s = 0; s < C::NG; ++s) {
+            mbar_init(&g_full[s], 1);
+            mbar_init(&g_empty[s], 1);
+        }
+        mbar_init(s_full, 1);
+        mbar_init(p_full, 8);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_full, 8);
+        mbar_init(dv_done, 1);
+        mbar_init(dk_done, 1);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    grid_wait();  // the lists, statistics and bias values below are the earlier kernels'
     if constexpr (BIAS) bias_table(sTab, a.tab, bh % a.H, a.buckets, threadIdx.x, kBwdThreads);
     int tc = 0;
     bool head_ok = true;
@@ -116,31 +142,6 @@ bwd_dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ Bwd
     }
     const int n = (count + NSUB - 1) / NSUB;
     auto qblock = [&](int x) { return WINDOW ? q_lo + x : __ldg(list + x); };
-
-    if (threadIdx.x == 0) {
-        mbar_init(kv_full, 1);
-        for (int s = 0; s < C::NQ; ++s) {
-            mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
-        }
-        for (int s = 0; s < C::NG; ++s) {
-            mbar_init(&g_full[s], 1);
-            mbar_init(&g_empty[s], 1);
-        }
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 8);
-        mbar_init(dp_full, 1);
-        mbar_init(ds_full, 8);
-        mbar_init(dv_done, 1);
-        mbar_init(dk_done, 1);
-        mbar_init(mma_done, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -576,8 +577,9 @@ vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention backward, dK and dV)");
-    kern<<<static_cast<unsigned>(a.nt) * a.BH, kBwdThreads, smem, st>>>(maps, a);
-    return check_cuda(cudaGetLastError(), "attention backward launch (dK and dV)");
+    return check_cuda(launch_kernel(true, kern, dim3(static_cast<unsigned>(a.nt) * a.BH), dim3(kBwdThreads), smem, st,
+                                    bwd_maps<TILED>(maps), a),
+                      "attention backward launch (dK and dV)");
 }
 
 template <int D>

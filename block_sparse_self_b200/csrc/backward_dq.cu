@@ -54,7 +54,7 @@ struct KeyWalk {
 
 template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
+bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, const __grid_constant__ BwdArgs a) {
     using C = DqCfg<D>;
     constexpr int SLAB = 128 * 128, NSUB = 128 / BS;
     extern __shared__ uint8_t smem_raw[];
@@ -75,7 +75,6 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qb = blockIdx.x, bh = blockIdx.y;
-    if constexpr (BIAS) bias_table(sTab, a.tab, bh % a.H, a.buckets, threadIdx.x, kBwdThreads);
     KeyWalk<WINDOW> w{};
     if constexpr (WINDOW) {
         const int q0 = qb * 128;
@@ -137,9 +136,14 @@ bwd_dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdA
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    grid_wait();  // what comes before reads the caller's lists only
+    if constexpr (BIAS) bias_table(sTab, a.tab, bh % a.H, a.buckets, threadIdx.x, kBwdThreads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // only now that this CTA has its tensor memory: a CTA of the dK/dV pass on this SM
+    // could take it first and would then wait for this one
+    grid_release();
     const uint32_t tmem = *tmem_slot;
     bool head_ok = true;
     int tc = 0;
@@ -511,9 +515,8 @@ vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention backward, dQ)");
-    dim3 grid(a.nt, a.BH);
-    kern<<<grid, kBwdThreads, smem, st>>>(maps, a);
-    return check_cuda(cudaGetLastError(), "attention backward launch (dQ)");
+    return check_cuda(launch_kernel(true, kern, dim3(a.nt, a.BH), dim3(kBwdThreads), smem, st, bwd_maps<TILED>(maps), a),
+                      "attention backward launch (dQ)");
 }
 
 template <int D>

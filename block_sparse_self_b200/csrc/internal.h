@@ -147,7 +147,8 @@ vsa_status launch_compensated(const AttnLaunch &a, void *workspace, int *status,
 // rows [lists, nb * cap]; `fill` writes -1 behind each list's last entry.
 size_t transpose_lists_workspace_bytes(int lists, int nb);
 cudaError_t launch_transpose_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap, int32_t *offsets,
-                                   int32_t *rows, bool fill, void *workspace, int *status, cudaStream_t st);
+                                   int32_t *rows, bool fill, void *workspace, int *status, bool chained,
+                                   cudaStream_t st);  // chained: see chain.cuh
 
 // Relative position bias (relative_bias.cu): values by head and bucket, and the
 // buckets of offsets -R .. R, R = bias_reach(S, far), in the workspace (*bm at

@@ -11,6 +11,7 @@
 // The attention kernels read bucket(r) as a byte, for |r| <= R = min(far, S)
 // (larger offsets fall into the last bucket of their side), and each head's
 // values tab[h][b] = log2(e) table[b][h].
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -56,6 +57,7 @@ template <typename T>
 __global__ void expand_kernel(const Borders b, const T *__restrict__ table, int H, int buckets, int R,
                               float *__restrict__ tab, uint8_t *__restrict__ bm) {
     const int x = blockIdx.x * 256 + threadIdx.x;
+    grid_release();
     if (x <= 2 * R) bm[x] = static_cast<uint8_t>(bucket_of(x - R, b));
     if (x < H * buckets) {
         const int h = x / buckets, k = x - h * buckets;
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(1024) dbias_kernel(const float *__restrict__ p
                                                      T *__restrict__ dtable) {
     __shared__ double sum[32][33];
     const int b = blockIdx.x * 32 + threadIdx.x, h = blockIdx.y;
+    grid_wait();
     double s = 0.0;
     if (b < buckets)
         for (int i = threadIdx.y; i < B * per; i += 32) {
@@ -118,11 +121,9 @@ cudaError_t launch_bias_buckets(int buckets, int far, int32_t *out, cudaStream_t
 cudaError_t launch_dbias(const float *part, int B, int H, int per, int buckets, void *dtable, bool f32,
                          cudaStream_t st) {
     const dim3 grid((buckets + 31) / 32, H), block(32, 32);
-    if (f32)
-        dbias_kernel<<<grid, block, 0, st>>>(part, B, H, per, buckets, static_cast<float *>(dtable));
-    else
-        dbias_kernel<<<grid, block, 0, st>>>(part, B, H, per, buckets, static_cast<__nv_bfloat16 *>(dtable));
-    return cudaGetLastError();
+    if (f32) return launch_kernel(true, dbias_kernel<float>, grid, block, 0, st, part, B, H, per, buckets, static_cast<float *>(dtable));
+    return launch_kernel(true, dbias_kernel<__nv_bfloat16>, grid, block, 0, st, part, B, H, per, buckets,
+                         static_cast<__nv_bfloat16 *>(dtable));
 }
 
 }  // namespace vsa

@@ -12,6 +12,7 @@
 // over the SMs.  What bounds both is latency (launches, then the lists' rows),
 // not bytes: 7 blocks take 4.4 us against 9.8, 120 blocks 11.5 against 16, but
 // 240 blocks 22 against 17 and 960 blocks 80 against 32 (kernel times).
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t *__restric
     extern __shared__ uint32_t word[];
     const int col = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t list = blockIdx.y;
+    grid_release();
     uint32_t *out = bits + (list * gridDim.x + col) * nb;
     for (int k0 = 0; k0 < nb; k0 += kKeysAtOnce) {
         const int keys = min(kKeysAtOnce, nb - k0);
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t *__restric
         for (int k = threadIdx.x; k < keys; k += 256) out[k0 + k] = word[k];
         __syncthreads();
     }
+    grid_wait();
 }
 
 // One CTA per list: offsets[k] = entries of the key blocks before k.
@@ -87,6 +90,8 @@ __global__ void __launch_bounds__(1024) list_offsets_kernel(const uint32_t *__re
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t *b = bits + list * cols * nb;
     int32_t *off = offsets + list * (nb + 1);
+    grid_release();
+    grid_wait();
     int before = 0;
     for (int k0 = 0; k0 < nb; k0 += 1024) {
         const int k = k0 + threadIdx.x;
@@ -127,6 +132,8 @@ __global__ void __launch_bounds__(256) list_rows_kernel(const uint32_t *__restri
                                                         int fill, int32_t *__restrict__ rows) {
     const int key = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const size_t list = blockIdx.y;
+    grid_release();
+    grid_wait();
     if (key >= nb) return;
     const uint32_t *b = bits + list * cols * nb + key;
     int32_t *out = rows + list * nb * cap;
@@ -166,6 +173,7 @@ __global__ void __launch_bounds__(1024) list_turn_kernel(const int32_t *__restri
     const int cols = (nb + 31) / 32, stride = one_cta_stride(nb);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t list = blockIdx.x;
+    grid_release();
     for (int e = threadIdx.x; e < cols * stride; e += 1024) word[e] = 0u;
     __syncthreads();
     for (int q = warp; q < nb; q += 32) {
@@ -226,6 +234,7 @@ __global__ void __launch_bounds__(1024) list_turn_kernel(const int32_t *__restri
     }
     if (fill)
         for (int e = before + threadIdx.x; e < nb * cap; e += 1024) out[e] = -1;
+    grid_wait();
 }
 
 }  // namespace
@@ -235,19 +244,21 @@ size_t transpose_lists_workspace_bytes(int lists, int nb) {
 }
 
 cudaError_t launch_transpose_lists(const int32_t *idx, const int32_t *cnt, int lists, int nb, int cap, int32_t *offsets,
-                                   int32_t *rows, bool fill, void *workspace, int *status, cudaStream_t st) {
+                                   int32_t *rows, bool fill, void *workspace, int *status, bool chained, cudaStream_t st) {
     const int cols = (nb + 31) / 32;
     if (nb <= kOneCtaBlocks) {
         const int smem = cols * one_cta_stride(nb) * 4;  // at most 2 KB
-        list_turn_kernel<<<lists, 1024, smem, st>>>(idx, cnt, nb, cap, offsets, rows, fill ? 1 : 0, status);
-        return cudaGetLastError();
+        return launch_kernel(chained, list_turn_kernel, dim3(lists), dim3(1024), smem, st, idx, cnt, nb, cap, offsets, rows,
+                             fill ? 1 : 0, status);
     }
     uint32_t *bits = static_cast<uint32_t *>(workspace);
-    list_bits_kernel<<<dim3(cols, lists), 256, (nb < kKeysAtOnce ? nb : kKeysAtOnce) * 4, st>>>(idx, cnt, nb, cap, bits,
-                                                                                              status);
-    list_offsets_kernel<<<lists, 1024, 0, st>>>(bits, nb, cols, offsets);
-    list_rows_kernel<<<dim3((nb + 7) / 8, lists), 256, 0, st>>>(bits, offsets, nb, cols, cap, fill ? 1 : 0, rows);
-    return cudaGetLastError();
+    cudaError_t e = launch_kernel(chained, list_bits_kernel, dim3(cols, lists), dim3(256),
+                                  (nb < kKeysAtOnce ? nb : kKeysAtOnce) * 4, st, idx, cnt, nb, cap, bits, status);
+    if (e == cudaSuccess) e = launch_kernel(true, list_offsets_kernel, dim3(lists), dim3(1024), 0, st, bits, nb, cols, offsets);
+    if (e == cudaSuccess)
+        e = launch_kernel(true, list_rows_kernel, dim3((nb + 7) / 8, lists), dim3(256), 0, st, bits, offsets, nb, cols, cap,
+                          fill ? 1 : 0, rows);
+    return e;
 }
 
 }  // namespace vsa
