@@ -146,11 +146,11 @@ _NO_GUARD = contextlib.nullcontext()
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        if t.is_contiguous():
+            return t
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be a CUDA tensor")
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -482,7 +482,7 @@ def _out_dtype(out_dtype, ref):
 
 def _qkv_shape(q, k, v):
     B, H, S, D = _bhsd(q, "q")
-    if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
+    if k.shape != q.shape or v.shape != q.shape:
         raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
                          f"v={tuple(v.shape)}")
     return B, H, S, D
@@ -505,13 +505,23 @@ def _check_lists(idx, cnt, B, H, nb):
 
 
 def _same_device(ref, **tensors):
+    index = ref.get_device()
     for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != ref.device:
+        if isinstance(t, torch.Tensor) and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, q on {ref.device}")
 
 
 def _code(dtype) -> int:
     return BF16 if dtype == torch.bfloat16 else F32
+
+
+def _like(t, dtype) -> torch.Tensor:
+    """An empty tensor of t's shape (t contiguous); torch.empty with sizes takes half as long again."""
+    return torch.empty_like(t) if t.dtype == dtype else torch.empty_like(t, dtype=dtype)
+
+
+def _bytes(n: int, ref) -> torch.Tensor:
+    return ref.new_empty(n, dtype=torch.uint8)
 
 
 def _scale(scale) -> float:
@@ -520,14 +530,13 @@ def _scale(scale) -> float:
 
 def _check_saved(do, q, o, lse, o_lo):
     """The forward pass's output and the gradient that comes back for it."""
-    B, H, S, D = q.shape
-    if tuple(do.shape) != (B, H, S, D) or tuple(o.shape) != (B, H, S, D):
-        raise ValueError(f"do and o must have q's shape {(B, H, S, D)}; got {tuple(do.shape)} and {tuple(o.shape)}")
+    if do.shape != q.shape or o.shape != q.shape:
+        raise ValueError(f"do and o must have q's shape {tuple(q.shape)}; got {tuple(do.shape)} and {tuple(o.shape)}")
     _cuda(o, "o")
     _dtype_code(o, "o")
     _cuda(lse, "lse")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, S):
-        raise ValueError(f"lse must be float32 of shape {(B, H, S)}, as the forward call returns it")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
+        raise ValueError(f"lse must be float32 of shape {tuple(q.shape[:-1])}, as the forward call returns it")
     if o_lo is not None:
         _cuda(o_lo, "o_lo")
         if o_lo.dtype != torch.bfloat16 or o.dtype != torch.bfloat16 or o_lo.shape != o.shape:
@@ -536,7 +545,7 @@ def _check_saved(do, q, o, lse, o_lo):
 
 def _saved_outputs(o, remainder: bool):
     """lse and, beside a bf16 o, its remainder if asked for: what a forward call writes for the backward pass."""
-    lse = torch.empty(o.shape[:-1], dtype=torch.float32, device=o.device)
+    lse = o.new_empty(o.shape[:-1], dtype=torch.float32)
     return lse, torch.empty_like(o) if remainder and o.dtype == torch.bfloat16 else None
 
 
@@ -546,18 +555,20 @@ def _saved(o, lse, o_lo, return_lse, return_remainder):
     return (o, lse) if return_lse else o
 
 
+def _grads_as(grads, dtypes):
+    return tuple(g if g.dtype == t else g.to(t) for g, t in zip(grads, dtypes))
+
+
 class _BlockSparse(torch.autograd.Function):
-    """block_sparse_attention and its tiled form: `kind` holds the two calls and their arguments."""
+    """block_sparse_attention and its tiled form: `fwd` and `bwd` are the two calls past the checks of q, k and
+    v, `rest` their arguments behind the lists."""
 
     @staticmethod
-    def forward(ctx, q, k, v, fwd, bwd, args, kw, out_dtype):
+    def forward(ctx, q, k, v, fwd, bwd, idx, cnt, choice, rest, out_dtype):
         qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-        o, lse, o_lo = fwd(qb, kb, vb, *args, out_dtype=_out_dtype(out_dtype, q), return_remainder=True, **kw)
-        tensors = [a for a in args if isinstance(a, torch.Tensor)]
-        ctx.where = [isinstance(a, torch.Tensor) for a in args]
-        ctx.rest = [a for a in args if not isinstance(a, torch.Tensor)]
-        ctx.bwd, ctx.kw, ctx.dtypes = bwd, kw, (q.dtype, k.dtype, v.dtype)
-        ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, *tensors)
+        o, lse, o_lo = fwd(qb, kb, vb, _out_dtype(out_dtype, q), True, idx, cnt, choice, *rest)
+        ctx.bwd, ctx.rest, ctx.dtypes = bwd, rest, (q.dtype, k.dtype, v.dtype)
+        ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, idx, cnt, choice)
         ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
         return o, lse, o_lo
@@ -566,14 +577,42 @@ class _BlockSparse(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, *_):
         if do is None:
-            return (None,) * 8
-        qb, kb, vb, o, lse, o_lo, *tensors = ctx.saved_tensors
-        tensors, rest = iter(tensors), iter(ctx.rest)
-        args = [next(tensors) if t else next(rest) for t in ctx.where]
-        f32 = any(t == torch.float32 for t in ctx.dtypes)
-        grads = ctx.bwd(do.contiguous(), qb, kb, vb, o, lse, *args, o_lo=o_lo,
-                        grad_dtype=torch.float32 if f32 else torch.bfloat16, **ctx.kw)
-        return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (None,) * 5
+            return (None,) * 10
+        qb, kb, vb, o, lse, o_lo, idx, cnt, choice = ctx.saved_tensors
+        grads = ctx.bwd(_bf16(do.contiguous(), "do"), qb, kb, vb, o, lse, o_lo,
+                        torch.float32 if torch.float32 in ctx.dtypes else torch.bfloat16, idx, cnt, choice, *ctx.rest)
+        return _grads_as(grads, ctx.dtypes) + (None,) * 7
+
+
+def _lists_forward(qb, kb, vb, odt, remainder, idx, cnt, _, block, group_size, scale):
+    B, H, S, D = qb.shape
+    _same_device(qb, k=kb, v=vb, idx=idx, cnt=cnt)
+    o = _like(qb, odt)
+    lse, o_lo = _saved_outputs(o, remainder)
+    with _on(qb):
+        _check(lib().vsa_block_sparse_attention_lse(
+            qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(odt), lse.data_ptr(), _ptr(o_lo), B, H, S,
+            D, block, idx.data_ptr(), cnt.data_ptr(), idx.shape[-1], 1 if idx.dim() == 4 else 0, group_size, scale,
+            _stream(qb.device)))
+    return o, lse, o_lo
+
+
+def _lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, _, block, group_size, scale):
+    B, H, S, D = qb.shape
+    if block not in (32, 64, 128) or S % block:
+        raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
+    _check_lists(idx, cnt, B, H, S // block)
+    _same_device(qb, idx=idx, cnt=cnt)
+    cap, per_head = idx.shape[-1], 1 if idx.dim() == 4 else 0
+    dq, dk, dv = _like(qb, gdt), _like(qb, gdt), _like(qb, gdt)
+    with _on(qb):
+        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, S, block, cap, per_head)
+        ws = _bytes(need, qb)
+        _check(lib().vsa_block_sparse_attention_backward(
+            gb.data_ptr(), qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(o.dtype), _ptr(o_lo),
+            lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _code(gdt), B, H, S, D, block, idx.data_ptr(),
+            cnt.data_ptr(), cap, per_head, group_size, scale, ws.data_ptr(), need, _stream(qb.device)))
+    return dq, dk, dv
 
 
 def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, scale: Optional[float] = None,
@@ -588,25 +627,20 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     recorded, blocks of 32 and 64 tokens run on a kernel of their own whose
     output is rounded differently.
     Differentiable in q, k and v; the lists are constants of the backward pass."""
-    if _wants_grad(q, k, v):
-        o, lse, o_lo = _BlockSparse.apply(q, k, v, block_sparse_attention, block_sparse_attention_backward,
-                                          (idx, cnt, block), dict(group_size=group_size, scale=scale), out_dtype)
-        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
-    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     _lists_arg(idx, cnt)
-    per_head = idx.dim() == 4
-    cap = idx.shape[-1]
-    o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
+    rest = (int(block), int(group_size), _scale(scale))
+    if _wants_grad(q, k, v):
+        return _saved(*_BlockSparse.apply(q, k, v, _lists_forward, _lists_backward, idx, cnt, None, rest, odt),
+                      return_lse, return_remainder)
+    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     if return_lse or return_remainder:
-        lse, o_lo = _saved_outputs(o, return_remainder)
-        with _on(q):
-            _check(lib().vsa_block_sparse_attention_lse(
-                _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), _ptr(o_lo), B, H, S, D, int(block),
-                _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size), _scale(scale),
-                _stream(q.device)))
-        return _saved(o, lse, o_lo, return_lse, return_remainder)
+        return _saved(*_lists_forward(qb, kb, vb, odt, return_remainder, idx, cnt, None, *rest), return_lse,
+                      return_remainder)
+    o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
+    cap = idx.shape[-1]
+    per_head = idx.dim() == 4
     _check(lib().vsa_block_sparse_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(block),
                                             _ptr(idx), _ptr(cnt), int(cap), 1 if per_head else 0, int(group_size),
                                             _scale(scale), _stream(q.device)))
@@ -617,25 +651,15 @@ def block_sparse_attention_backward(do, q, k, v, o, lse, idx, cnt, block: int, g
                                     scale: Optional[float] = None, grad_dtype=None,
                                     o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention for the gradient `do` of its output, from that output
-    and its lse (and its remainder o_lo, if the forward call returned one).  The gradients have q's type unless grad_dtype says otherwise."""
-    B, H, S, D = _qkv_shape(q, k, v)
+    and its lse (and its remainder o_lo, if the forward call returned one).  The gradients have q's
+    type unless grad_dtype says otherwise."""
+    _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
     _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
-    if block not in (32, 64, 128) or S % block:
-        raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
-    _check_lists(idx, cnt, B, H, S // block)
-    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt)
-    cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
-    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
-    with _on(q):
-        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, S, int(block), cap, per_head)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(lib().vsa_block_sparse_attention_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-            _code(gdt), B, H, S, D, int(block), _ptr(idx), _ptr(cnt), cap, per_head, int(group_size), _scale(scale),
-            _ptr(ws), need, _stream(q.device)))
-    return dq, dk, dv
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo)
+    return _lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, None, int(block), int(group_size),
+                           _scale(scale))
 
 
 def transpose_block_lists(idx, cnt):
@@ -649,11 +673,10 @@ def transpose_block_lists(idx, cnt):
         raise ValueError(f"cnt is on {cnt.device}, idx on {idx.device}")
     lead, (nb, cap) = idx.shape[:-2], idx.shape[-2:]
     lists = math.prod(lead)
-    offsets = torch.empty(*lead, nb + 1, dtype=torch.int32, device=idx.device)
-    rows = torch.empty(*lead, nb * cap, dtype=torch.int32, device=idx.device)
+    offsets, rows = idx.new_empty((*lead, nb + 1)), idx.new_empty((*lead, nb * cap))
     with _on(idx):
         need = lib().vsa_transpose_block_lists_workspace_size(lists, nb)
-        ws = torch.empty(need, dtype=torch.uint8, device=idx.device) if need else None
+        ws = _bytes(need, idx) if need else None
         _check(lib().vsa_transpose_block_lists(_ptr(idx), _ptr(cnt), lists, nb, cap, _ptr(offsets), _ptr(rows),
                                                _ptr(ws), need, _stream(idx.device)))
     return offsets, rows
@@ -716,6 +739,42 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
     return o
 
 
+def _tiled_lists_forward(qb, kb, vb, odt, remainder, idx, cnt, choice, grid, tiles, group_stride, scale):
+    B, H, S, D = qb.shape
+    _same_device(qb, k=kb, v=vb, idx=idx, cnt=cnt, choice=choice)
+    arr, n = _tiles_arg(tiles)
+    o = _like(qb, odt)
+    lse, o_lo = _saved_outputs(o, remainder)
+    with _on(qb):
+        _check(lib().vsa_block_sparse_attention_tiled_lse(
+            qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(odt), lse.data_ptr(), _ptr(o_lo), B, H, S,
+            D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), idx.data_ptr(), cnt.data_ptr(), idx.shape[-1],
+            1 if idx.dim() == 4 else 0, group_stride, scale, _stream(qb.device)))
+    return o, lse, o_lo
+
+
+def _tiled_lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, choice, grid, tiles, group_stride, scale):
+    B, H, S, D = qb.shape
+    arr, n = _tiles_arg(tiles)
+    positions = _grid_tokens(padded_grid(grid, tiles))
+    block = min(128, math.prod(int(x) for x in tiles[0]))
+    if block not in (32, 64, 128) or positions % block:
+        raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {math.prod(tiles[0])}")
+    _check_lists(idx, cnt, B, H, positions // block)
+    _same_device(qb, idx=idx, cnt=cnt, choice=choice)
+    cap, per_head = idx.shape[-1], 1 if idx.dim() == 4 else 0
+    dq, dk, dv = _like(qb, gdt), _like(qb, gdt), _like(qb, gdt)
+    with _on(qb):
+        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, positions, block, cap, per_head)
+        ws = _bytes(need, qb)
+        _check(lib().vsa_block_sparse_attention_tiled_backward(
+            gb.data_ptr(), qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(o.dtype), _ptr(o_lo),
+            lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _code(gdt), B, H, S, D, Dims3(*grid), arr, n,
+            _choice_arg(choice, B * H), idx.data_ptr(), cnt.data_ptr(), cap, per_head, group_stride, scale,
+            ws.data_ptr(), need, _stream(qb.device)))
+    return dq, dk, dv
+
+
 def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: Optional[float] = None,
                                  out_dtype=None, group_stride: int = 0, return_lse: bool = False,
                                  return_remainder: bool = False):
@@ -725,26 +784,23 @@ def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: 
     group_stride s > 0 (128-token blocks) restricts each query to keys whose position
     differs from its own by a multiple of s (see include/vsa.h).  return_lse,
     return_remainder and differentiability as for block_sparse_attention; all in T-major order."""
-    if _wants_grad(q, k, v):
-        o, lse, o_lo = _BlockSparse.apply(q, k, v, block_sparse_attention_tiled, block_sparse_attention_tiled_backward,
-                                          (grid, tiles, choice, idx, cnt),
-                                          dict(scale=scale, group_stride=group_stride), out_dtype)
-        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
-    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
     _lists_arg(idx, cnt)
+    rest = (grid, tiles, int(group_stride), _scale(scale))
+    if _wants_grad(q, k, v):
+        return _saved(*_BlockSparse.apply(q, k, v, _tiled_lists_forward, _tiled_lists_backward, idx, cnt, choice, rest,
+                                          odt), return_lse, return_remainder)
+    qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
+    if return_lse or return_remainder:
+        return _saved(*_tiled_lists_forward(qb, kb, vb, odt, return_remainder, idx, cnt, choice, *rest), return_lse,
+                      return_remainder)
     arr, n = _tiles_arg(tiles)
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
-    tail = (B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), int(idx.shape[-1]),
-            1 if idx.dim() == 4 else 0, int(group_stride), _scale(scale), _stream(q.device))
-    if return_lse or return_remainder:
-        lse, o_lo = _saved_outputs(o, return_remainder)
-        with _on(q):
-            _check(lib().vsa_block_sparse_attention_tiled_lse(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt),
-                                                              _ptr(lse), _ptr(o_lo), *tail))
-        return _saved(o, lse, o_lo, return_lse, return_remainder)
-    _check(lib().vsa_block_sparse_attention_tiled(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), *tail))
+    _check(lib().vsa_block_sparse_attention_tiled(
+        _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H),
+        _ptr(idx), _ptr(cnt), int(idx.shape[-1]), 1 if idx.dim() == 4 else 0, int(group_stride), _scale(scale),
+        _stream(q.device)))
     return o
 
 
@@ -752,28 +808,15 @@ def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choi
                                           scale: Optional[float] = None, group_stride: int = 0, grad_dtype=None,
                                           o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention_tiled, all in T-major order, for the gradient `do` of its
-    output, from that output and its lse (and its remainder o_lo, if there is one).  The gradients have q's type unless grad_dtype says otherwise."""
-    B, H, S, D = _qkv_shape(q, k, v)
+    output, from that output and its lse (and its remainder o_lo, if there is one).  The gradients
+    have q's type unless grad_dtype says otherwise."""
+    _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
     _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
-    arr, n = _tiles_arg(tiles)
-    positions = _grid_tokens(padded_grid(grid, tiles))
-    block = min(128, math.prod(int(x) for x in tiles[0]))
-    if block not in (32, 64, 128) or positions % block:
-        raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {math.prod(tiles[0])}")
-    _check_lists(idx, cnt, B, H, positions // block)
-    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, idx=idx, cnt=cnt, choice=choice)
-    cap, per_head = int(idx.shape[-1]), 1 if idx.dim() == 4 else 0
-    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
-    with _on(q):
-        need = lib().vsa_block_sparse_attention_backward_workspace_size(B, H, positions, block, cap, per_head)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(lib().vsa_block_sparse_attention_tiled_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-            _code(gdt), B, H, S, D, Dims3(*grid), arr, n, _choice_arg(choice, B * H), _ptr(idx), _ptr(cnt), cap,
-            per_head, int(group_stride), _scale(scale), _ptr(ws), need, _stream(q.device)))
-    return dq, dk, dv
+    _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo)
+    return _tiled_lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, choice, grid, tiles, int(group_stride),
+                                 _scale(scale))
 
 
 def tiled_supported(tiles) -> bool:
@@ -801,11 +844,10 @@ def _bias_arg(bias, H):
 
 class _Window(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, bias, window, kw, out_dtype):
+    def forward(ctx, q, k, v, bias, args, out_dtype):
         qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-        o, lse, o_lo = window_attention(qb, kb, vb, window, out_dtype=_out_dtype(out_dtype, q), bias=bias,
-                                        return_remainder=True, **kw)
-        ctx.window, ctx.kw, ctx.dtypes = window, kw, (q.dtype, k.dtype, v.dtype)
+        o, lse, o_lo = _window_forward(qb, kb, vb, out_dtype, True, True, bias, *args)
+        ctx.args, ctx.dtypes = args, (q.dtype, k.dtype, v.dtype)
         ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, bias)
         ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
@@ -815,15 +857,46 @@ class _Window(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, *_):
         if do is None:
-            return (None,) * 7
+            return (None,) * 6
         qb, kb, vb, o, lse, o_lo, bias = ctx.saved_tensors
-        f32 = any(t == torch.float32 for t in ctx.dtypes)
-        kw = {n: x for n, x in ctx.kw.items() if n != "chunk_size"}
-        grads = window_attention_backward(do.contiguous(), qb, kb, vb, o, lse, ctx.window, bias=bias,
-                                          grad_dtype=torch.float32 if f32 else torch.bfloat16,
-                                          bias_grad=ctx.needs_input_grad[3], o_lo=o_lo, **kw)
-        dbias = grads[3] if ctx.needs_input_grad[3] else None
-        return tuple(g.to(t) for g, t in zip(grads, ctx.dtypes)) + (dbias, None, None, None)
+        *grads, dbias = _window_backward(_bf16(do.contiguous(), "do"), qb, kb, vb, o, lse, o_lo,
+                                         torch.float32 if torch.float32 in ctx.dtypes else torch.bfloat16, bias,
+                                         ctx.needs_input_grad[3], *ctx.args)
+        return _grads_as(grads, ctx.dtypes) + (dbias, None, None)
+
+
+def _window_forward(qb, kb, vb, odt, save, remainder, bias, window, sink, max_distance, scale):
+    B, H, S, D = qb.shape
+    _same_device(qb, k=kb, v=vb, bias=bias)
+    o = _like(qb, odt)
+    lse, o_lo = _saved_outputs(o, remainder) if save else (None, None)
+    buckets, need, ws = 0, 0, None
+    with _on(qb):
+        if bias is not None:
+            buckets = _bias_arg(bias, H)
+            need = lib().vsa_window_attention_lse_workspace_size(H, S, buckets, max_distance)
+            ws = _bytes(max(need, 1), qb)
+        _check(lib().vsa_window_attention_lse(
+            qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(odt), _ptr(lse), _ptr(o_lo), B, H, S, D,
+            window, sink, scale, _ptr(bias), F32 if bias is None else _code(bias.dtype), buckets, max_distance,
+            _ptr(ws), need, _stream(qb.device)))
+    return o, lse, o_lo
+
+
+def _window_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, bias, bias_grad, window, sink, max_distance, scale):
+    B, H, S, D = qb.shape
+    buckets = 0 if bias is None else _bias_arg(bias, H)
+    dq, dk, dv = _like(qb, gdt), _like(qb, gdt), _like(qb, gdt)
+    dbias = None if bias is None or not bias_grad else torch.empty_like(bias)
+    with _on(qb):
+        need = lib().vsa_window_attention_backward_workspace_size(B, H, S, buckets, max_distance)
+        ws = _bytes(max(need, 1), qb)
+        _check(lib().vsa_window_attention_backward(
+            gb.data_ptr(), qb.data_ptr(), kb.data_ptr(), vb.data_ptr(), o.data_ptr(), _code(o.dtype), _ptr(o_lo),
+            lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _code(gdt), B, H, S, D, window, sink, scale,
+            _ptr(bias), F32 if bias is None else _code(bias.dtype), buckets, max_distance, _ptr(dbias), ws.data_ptr(),
+            need, _stream(qb.device)))
+    return dq, dk, dv, dbias
 
 
 def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float] = None,
@@ -836,58 +909,38 @@ def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float]
     j of head h, with the buckets of relative_position_buckets(num_buckets,
     max_distance).  return_lse and return_remainder as for block_sparse_attention.
     Differentiable in q, k, v and bias."""
-    if _wants_grad(q, k, v, bias):
-        kw = dict(sink=sink, scale=scale, chunk_size=chunk_size, max_distance=max_distance)
-        o, lse, o_lo = _Window.apply(q, k, v, bias, window, kw, out_dtype)
-        return _saved(o, lse, o_lo, return_lse, return_remainder)
     B, H, S, D = _qkv_shape(q, k, v)
     if chunk_size is not None and int(chunk_size) < 1:
         raise ValueError(f"chunk_size must be >= 1, got {chunk_size}")
     odt = _out_dtype(out_dtype, q)
+    if _wants_grad(q, k, v, bias):
+        args = (int(window), int(sink), int(max_distance), _scale(scale))
+        return _saved(*_Window.apply(q, k, v, bias, args, odt), return_lse, return_remainder)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-    o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     if bias is None and not (return_lse or return_remainder):
+        o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
         _check(lib().vsa_window_attention(_ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), B, H, S, D, int(window),
                                           int(sink), _scale(scale), 0 if chunk_size is None else int(chunk_size),
                                           _stream(q.device)))
         return o
-    lse, o_lo = _saved_outputs(o, return_remainder) if return_lse or return_remainder else (None, None)
-    buckets, need, ws = 0, 0, None
-    _same_device(q, k=k, v=v, bias=bias)
-    with _on(q):
-        if bias is not None:
-            buckets = _bias_arg(bias, H)
-            need = lib().vsa_window_attention_lse_workspace_size(H, S, buckets, int(max_distance))
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        _check(lib().vsa_window_attention_lse(
-            _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(odt), _ptr(lse), _ptr(o_lo), B, H, S, D, int(window), int(sink),
-            _scale(scale), _ptr(bias), F32 if bias is None else _code(bias.dtype), buckets, int(max_distance),
-            _ptr(ws), need, _stream(q.device)))
-    return _saved(o, lse, o_lo, return_lse, return_remainder)
+    return _saved(*_window_forward(qb, kb, vb, odt, return_lse or return_remainder, return_remainder, bias, int(window),
+                                   int(sink), int(max_distance), _scale(scale)), return_lse, return_remainder)
 
 
 def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, scale: Optional[float] = None,
                               bias: Optional[torch.Tensor] = None, max_distance: int = 128, grad_dtype=None,
                               bias_grad: bool = True, o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of window_attention for the gradient `do` of its output, from that output and its
-    lse (and its remainder o_lo, if there is one); with a bias (dq, dk, dv, dbias), dbias in the bias's type, or None with bias_grad=False.
-    The gradients of q, k and v have q's type unless grad_dtype says otherwise."""
-    B, H, S, D = _qkv_shape(q, k, v)
+    lse (and its remainder o_lo, if there is one); with a bias (dq, dk, dv, dbias), dbias in the
+    bias's type, or None with bias_grad=False.  The gradients of q, k and v have q's type unless
+    grad_dtype says otherwise."""
+    _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
     _check_saved(do, q, o, lse, o_lo)
     qb, kb, vb, gb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(do, "do")
     _same_device(q, k=k, v=v, do=do, o=o, lse=lse, o_lo=o_lo, bias=bias)
-    buckets = 0 if bias is None else _bias_arg(bias, H)
-    dq, dk, dv = (torch.empty(B, H, S, D, dtype=gdt, device=q.device) for _ in range(3))
-    dbias = None if bias is None or not bias_grad else torch.empty_like(bias)
-    with _on(q):
-        need = lib().vsa_window_attention_backward_workspace_size(B, H, S, buckets, int(max_distance))
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        _check(lib().vsa_window_attention_backward(
-            _ptr(gb), _ptr(qb), _ptr(kb), _ptr(vb), _ptr(o), _code(o.dtype), _ptr(o_lo), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-            _code(gdt), B, H, S, D, int(window), int(sink), _scale(scale), _ptr(bias),
-            F32 if bias is None else _code(bias.dtype), buckets, int(max_distance), _ptr(dbias), _ptr(ws), need,
-            _stream(q.device)))
+    dq, dk, dv, dbias = _window_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, bias, bias_grad, int(window), int(sink),
+                                         int(max_distance), _scale(scale))
     return (dq, dk, dv) if bias is None else (dq, dk, dv, dbias)
 
 
