@@ -122,24 +122,33 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     grid_wait();
 }
 
-// kmean[bh][t][d]: the mean of the keys of tile t (of its rows that exist).  One
-// CTA per tile: thread (g, c) sums 8 columns of every (2048 / D)-th row; the rows' sums
-// are joined in a fixed order.  Bandwidth bound: K read once.
-template <int D>
-__global__ void __launch_bounds__(256) tile_means_kernel(const __nv_bfloat16 *__restrict__ k, int S, int nt,
-                                                         float *__restrict__ kmean) {
+// kmean[bh][t][d]: the mean of the keys of block t (of its rows that hold one; 0
+// if none does).  One CTA per block: thread (g, c) sums 8 columns of every (2048 / D)-th
+// row; the rows' sums are joined in a fixed order.  Bandwidth bound: K read once.
+template <int D, int BS>
+__global__ void __launch_bounds__(256) block_means_kernel(const __grid_constant__ StatArgs a,
+                                                          const __nv_bfloat16 *__restrict__ k, int nt,
+                                                          float *__restrict__ kmean) {
     constexpr int CH = D / 8, GROUPS = 256 / CH;
     __shared__ float part[GROUPS][D + 8];
     const int t = blockIdx.x, bh = blockIdx.y, c = threadIdx.x % CH, g = threadIdx.x / CH;
-    const int rows = min(128, S - t * 128);
     grid_release();
+    int tc = a.tiled && a.choice ? __ldg(a.choice + bh) : 0;
+    if (tc < 0 || tc >= a.n_tiles) tc = 0;  // the head is not computed
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const __nv_bfloat16 *src = k + (static_cast<size_t>(bh) * S + static_cast<size_t>(t) * 128) * D + c * 8;
+    int rows = 0;
     #pragma unroll
-    for (int i = 0; i < 128 / GROUPS; ++i) {
-        const int r = i * GROUPS + g;
-        if (r < rows) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<size_t>(r) * D));
+    for (int i = 0; i < BS / GROUPS; ++i) {
+        const int p = t * BS + i * GROUPS + g;
+        int tok = p < a.P ? p : -1;
+        if (a.tiled && tok >= 0) {
+            uint32_t ft, fh, fw;
+            tile_coords_fast(p, a.divs[tc], ft, fh, fw);
+            tok = real_token(ft, fh, fw, a.real);
+        }
+        if (tok >= 0) {
+            ++rows;
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(k + (static_cast<size_t>(bh) * a.S_out + tok) * D + c * 8));
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -150,11 +159,15 @@ __global__ void __launch_bounds__(256) tile_means_kernel(const __nv_bfloat16 *__
     }
     #pragma unroll
     for (int e = 0; e < 8; ++e) part[g][c * 8 + e] = s[e];
+    if (c == 0) part[g][D] = static_cast<float>(rows);
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 256) {
-        float x = 0.f;
-        for (int y = 0; y < GROUPS; ++y) x += part[y][d];
-        kmean[(static_cast<size_t>(bh) * nt + t) * D + d] = x / rows;
+        float x = 0.f, n = 0.f;
+        for (int y = 0; y < GROUPS; ++y) {
+            x += part[y][d];
+            n += part[y][D];
+        }
+        kmean[(static_cast<size_t>(bh) * nt + t) * D + d] = n > 0.f ? x / n : 0.f;
     }
     grid_wait();
 }
@@ -164,6 +177,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Layout {
     size_t nlse, ndelta, none, valid, kmean, t_off, t_rows, bits, part, bias, total;
 };
+
+// Whether dQ's rows are centered (backward_dq.cu says what it costs and brings):
+// windows always, lists where they hold at most 8 blocks.
+constexpr int kCenterBlocks = 8;
+bool centered(int lists, int cap) { return lists == 0 || cap <= kCenterBlocks; }
 
 Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far) {
     const size_t Pw = (static_cast<size_t>(positions) + 127) / 128 * 128;
@@ -178,7 +196,7 @@ Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, i
     L.ndelta = take(BH * Pw * 4);
     L.none = take(256 * 4);
     L.valid = take(BH * (Pw / 32) * 4);
-    if (lists == 0) L.kmean = take(BH * (Pw / 128) * 128 * 4);  // D <= 128
+    if (centered(lists, cap)) L.kmean = take(BH * (lists > 0 ? nb : Pw / 128) * 128 * 4);  // D <= 128
     if (lists > 0) {
         L.t_off = take(static_cast<size_t>(lists) * (nb + 1) * 4);
         L.t_rows = take(static_cast<size_t>(lists) * nb * cap * 4);
@@ -281,8 +299,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
 
-    // one chain of launches (see chain.cuh): bias values and tile means (windows), row
-    // statistics, transposed lists, dQ, dK and dV, the bias's gradient
+    // one chain of launches (see chain.cuh): bias values, mean keys, row statistics, transposed lists, dQ, dK and dV, the bias's gradient
     if (buckets > 0) {
         const vsa_status r = check_cuda(launch_bias_expand(B.bias, B.bias_f32, B.H, L.S, buckets, B.far, ws + lay.bias,
                                                            &a.tab, &a.bm, st),
@@ -292,20 +309,20 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
         a.buckets = buckets;
         a.dbias_part = B.dbias ? f32_at(lay.part) : nullptr;
     }
-    if (L.window) {
+    if (centered(lists, L.cap)) {
         float *kmean = f32_at(lay.kmean);
-        const dim3 tiles(a.nt, L.BH);
-        const auto *k = static_cast<const __nv_bfloat16 *>(L.k);
-        const vsa_status r = check_cuda(launch_kernel(buckets > 0, L.D == 128 ? tile_means_kernel<128> : tile_means_kernel<64>,
-                                                      tiles, dim3(256), 0, st, k, L.S, a.nt, kmean),
-                                        "attention backward launch (tile means)");
+        auto means = L.D == 128 ? (L.block == 128 ? block_means_kernel<128, 128> : L.block == 64 ? block_means_kernel<128, 64> : block_means_kernel<128, 32>)
+                                : (L.block == 128 ? block_means_kernel<64, 128> : L.block == 64 ? block_means_kernel<64, 64> : block_means_kernel<64, 32>);
+        const vsa_status r = check_cuda(launch_kernel(buckets > 0, means, dim3(a.nt, L.BH), dim3(256), 0, st, s,
+                                                      static_cast<const __nv_bfloat16 *>(L.k), a.nt, kmean),
+                                        "attention backward launch (mean keys)");
         if (r != VSA_OK) return r;
         a.kmean = kmean;
     }
     const dim3 grid((a.Pw / 32 + 7) / 8, L.BH);
     auto row_stats = L.D == 128 ? (B.o_f32 ? row_stats_kernel<128, true> : row_stats_kernel<128, false>)
                                 : (B.o_f32 ? row_stats_kernel<64, true> : row_stats_kernel<64, false>);
-    vsa_status r = check_cuda(launch_kernel(L.window, row_stats, grid, dim3(256), 0, st, s),
+    vsa_status r = check_cuda(launch_kernel(a.kmean != nullptr, row_stats, grid, dim3(256), 0, st, s),
                               "attention backward launch (row statistics)");
     if (r != VSA_OK) return r;
     if (lists > 0) {

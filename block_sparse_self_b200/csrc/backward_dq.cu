@@ -12,18 +12,19 @@
 // from, so the next tile's S is computed while this one is worked on, and dP
 // is refilled as soon as it has been read.
 //
-// Windows: the keys of a window often have a mean far larger than their spread
-// (neighbouring positions are alike), and then dQ, which only depends on the
-// spread since sum_j dX_ij = 0, drowns in that mean times the errors of dX.  So
-// the row's sum of dX as the MMA got it, times a vector close to its mean key,
-// is taken off again at the end:
+// Windows and short lists (CENTER): the keys that a row sees often have a mean far
+// larger than their spread (neighbouring positions are alike), and then dQ, which
+// only depends on the spread since sum_j dX_ij = 0, drowns in that mean times the
+// errors of dX.  So the row's sum of dX as the MMA got it, times a vector close to
+// its mean key, is taken off again at the end:
 //   dQ_i = scale (sum_j dX_ij k_j - (sum_j dX_ij) c),
-// an identity for any c.  c is, per 32 rows, the mean key of every tile weighted
-// with the mass of P in it (from a quarter of the columns).  With it dQ's error
-// against 64 bits falls from 4.1e-3 to 2.6e-3 of its norm (window 4096, S = 16384), from
-// 4.6e-3 to 2.6e-3 (window 159, S = 2048; 1.7e-3 is the rounding to bf16).  Block lists
-// reach over the whole grid, the tiles' means say little there (2.77e-3 to
-// 2.76e-3), and they go without.
+// an identity for any c.  c is, per 32 rows, the mean key of every block (windows:
+// tile of 128) weighted with the mass of P in it (from a quarter of the columns).
+// With it dQ's error against 64 bits falls from 4.1e-3 to 2.6e-3 of its norm (window
+// 4096, S = 16384), from 4.6e-3 to 2.6e-3 (window 159, S = 2048; 1.7e-3 is the rounding
+// to bf16), from 4.8e-3 to 3.0e-3 (3 of 1080 blocks of 32, o in bf16 without its remainder).
+// Longer lists average over the whole grid: 14 of 120 blocks of 64 go from 3.50e-3
+// to 3.43e-3 and would pay 228 -> 253 us for it, so lists of more than 8 go without.
 #include "backward.cuh"
 
 namespace vsa {
@@ -52,7 +53,8 @@ struct KeyWalk {
     }
 };
 
-template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
+// CENTER: the rows' sums of dX are taken off (see above).
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS, bool CENTER>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, const __grid_constant__ BwdArgs a) {
     using C = DqCfg<D>;
@@ -289,8 +291,8 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
             nd = __ldg(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
         }
         float row_sum[2] = {0.f, 0.f};
-        // windows: the row's sum of dX as rounded, the mass of P in this warp's
-        // columns, and sum over the tiles of mass times mean key (columns CPL lane ..)
+        // CENTER: the row's sum of dX as rounded, the mass of P in this warp's
+        // columns, and sum over the blocks of mass times mean key (columns CPL lane ..)
         constexpr int CPL = D / 32;
         [[maybe_unused]] float used_sum[2] = {0.f, 0.f}, mass = 0.f, center[CPL];
         #pragma unroll
@@ -346,11 +348,17 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
             float pr[64];
-            [[maybe_unused]] float mean[CPL];
-            if constexpr (WINDOW) {
-                const float *km = a.kmean + (static_cast<size_t>(bh) * a.nt + w.at(j)) * D + CPL * lane;
+            // blocks in this warp's 64 columns (of blocks of 128, half of one)
+            constexpr int NB = BS < 64 ? 64 / BS : 1;
+            [[maybe_unused]] float mean[NB][CPL];
+            if constexpr (CENTER) {
                 #pragma unroll
-                for (int e = 0; e < CPL; ++e) mean[e] = __ldg(km + e);
+                for (int b = 0; b < NB; ++b) {
+                    const int x = WINDOW ? j : min(j * NSUB + 64 * hf / BS + b, w.count - 1);
+                    const float *km = a.kmean + (static_cast<size_t>(bh) * a.nt + w.at(x)) * D + CPL * lane;
+                    #pragma unroll
+                    for (int e = 0; e < CPL; ++e) mean[b][e] = __ldg(km + e);
+                }
             }
             {
                 uint32_t x[64];
@@ -399,16 +407,19 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                 #pragma unroll
                 for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(__uint_as_float(x[c]));
             }
-            if constexpr (WINDOW) {
-                float m = 0.f;
+            if constexpr (CENTER) {
                 #pragma unroll
-                for (int c = 0; c < 64; c += 4) m += pr[c];
-                m = m < 1e30f ? m : 0.f;  // a row that is not finite must not reach its neighbours
-                #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-                mass += m;
-                #pragma unroll
-                for (int e = 0; e < CPL; ++e) center[e] = fmaf(m, mean[e], center[e]);
+                for (int b = 0; b < NB; ++b) {
+                    float m = 0.f;
+                    #pragma unroll
+                    for (int c = 64 / NB * b; c < 64 / NB * (b + 1); c += 4) m += pr[c];
+                    m = m < 1e30f ? m : 0.f;  // a row that is not finite must not reach its neighbours
+                    #pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+                    mass += m;
+                    #pragma unroll
+                    for (int e = 0; e < CPL; ++e) center[e] = fmaf(m, mean[b][e], center[e]);
+                }
             }
             if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
@@ -429,7 +440,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                         row_sum[0] += d0;
                         row_sum[1] += d1;
                         const uint32_t pk = pack_bf16x2(d0, d1);  // bf16: the type of the MMA's operand
-                        if constexpr (WINDOW) add_bf16x2_f32(pk, used_sum[0], used_sum[1]);
+                        if constexpr (CENTER) add_bf16x2_f32(pk, used_sum[0], used_sum[1]);
                         dsk[16 * u + (c >> 1)] = pk;
                     }
                 }
@@ -459,10 +470,10 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
             have = false;
             if (!*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
         }
-        // windows: sums and weighted means of the two halves of the columns meet in
+        // CENTER: sums and weighted means of the two halves of the columns meet in
         // the K ring, which nothing reads or fills any more
         float *sUsed = reinterpret_cast<float *>(sK), *sMean = sUsed + 256;  // [2][128], [8][D + 1]
-        if constexpr (WINDOW) {
+        if constexpr (CENTER) {
             if (have) {
                 sUsed[hf * 128 + row] = used_sum[0] + used_sum[1];
                 #pragma unroll
@@ -476,7 +487,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                 tc_fence_after();
                 [[maybe_unused]] float used = 0.f;
                 [[maybe_unused]] const float *c0 = sMean + wq * (D + 1), *c1 = sMean + (wq + 4) * (D + 1);
-                if constexpr (WINDOW) {
+                if constexpr (CENTER) {
                     const float total = c0[D] + c1[D];
                     used = total > 0.f ? (sUsed[row] + sUsed[128 + row]) / total : 0.f;
                 }
@@ -486,7 +497,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                     const int col = hf * (D / 2) + 32 * c;
                     tmem_ld32(t_lane + C::DQ_COL + col, x);
                     tmem_ld_wait();
-                    if constexpr (WINDOW) {
+                    if constexpr (CENTER) {
                         #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             x[e] = __float_as_uint(fmaf(-used, c0[col + e] + c1[col + e], __uint_as_float(x[e])));
@@ -507,10 +518,10 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
     }
 }
 
-template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS, bool CENTER>
 vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     using C = DqCfg<D>;
-    auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS>;
+    auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS, CENTER>;
     constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -519,15 +530,19 @@ vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
                       "attention backward launch (dQ)");
 }
 
+template <int D, bool TILED, bool CENTER>
+vsa_status pick_lists(const BwdMaps &maps, const BwdArgs &a, int block, cudaStream_t st) {
+    if (block == 128) return run<D, 128, false, TILED, false, CENTER>(maps, a, st);
+    return block == 64 ? run<D, 64, false, TILED, false, CENTER>(maps, a, st)
+                       : run<D, 32, false, TILED, false, CENTER>(maps, a, st);
+}
+
 template <int D>
 vsa_status pick(const BwdMaps &maps, const BwdArgs &a, int block, bool window, bool tiled, bool bias, cudaStream_t st) {
-    if (window) return bias ? run<D, 128, true, false, true>(maps, a, st) : run<D, 128, true, false, false>(maps, a, st);
-    if (tiled) {
-        if (block == 128) return run<D, 128, false, true, false>(maps, a, st);
-        return block == 64 ? run<D, 64, false, true, false>(maps, a, st) : run<D, 32, false, true, false>(maps, a, st);
-    }
-    if (block == 128) return run<D, 128, false, false, false>(maps, a, st);
-    return block == 64 ? run<D, 64, false, false, false>(maps, a, st) : run<D, 32, false, false, false>(maps, a, st);
+    if (window)
+        return bias ? run<D, 128, true, false, true, true>(maps, a, st) : run<D, 128, true, false, false, true>(maps, a, st);
+    if (a.kmean) return tiled ? pick_lists<D, true, true>(maps, a, block, st) : pick_lists<D, false, true>(maps, a, block, st);
+    return tiled ? pick_lists<D, true, false>(maps, a, block, st) : pick_lists<D, false, false>(maps, a, block, st);
 }
 
 }  // namespace

@@ -775,6 +775,67 @@ def test_window_gradients_of_keys_with_a_large_mean(S, window, sink):
     assert (dq[0, 0].double() - ref["dq"]).norm() <= 0.05 * rough
 
 
+def check_large_mean(dq, q, k, v, g, see):
+    """As for the windows above: dq's errors multiply the keys' spread."""
+    S, D = q.shape
+    ref = reference(q, k, v, g, see)
+    k64 = k.double()
+    spread = (k64.amax(0) - k64.amin(0))[None, :]
+    scale = 1 / math.sqrt(D)
+    bound = scale * (ref["e_dX"].sum(1, keepdim=True) * spread
+                     + S * 2.0 ** -24 * ref["dX"].abs().sum(1, keepdim=True) * k64.abs().amax(0)[None, :])
+    assert ((dq.double() - ref["dq"]).abs() <= bound + 1e-5).all()
+    rough = (scale * ref["e_dX"] @ k64.abs()).norm()
+    assert (dq.double() - ref["dq"]).norm() <= 0.05 * rough
+
+
+def large_mean_inputs(H, S, D):
+    q, k, v, g = inputs(1, H, S, D, seed=S + D)
+    m = torch.randn(1, H, 1, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    return (q.float() * 0.1).bfloat16(), (k.float() * 0.25 + 8 * m).bfloat16(), v, g
+
+
+@pytest.mark.parametrize("block,nb,D,longest,group", [(32, 9, 64, 3, 0), (32, 11, 128, 8, 0), (64, 7, 64, 5, 0),
+                                                      (64, 6, 128, 1, 0), (128, 5, 128, 3, 0), (128, 4, 64, 2, 64)])
+def test_short_lists_gradients_of_keys_with_a_large_mean(block, nb, D, longest, group):
+    H = 2
+    q, k, v, g = large_mean_inputs(H, block * nb, D)
+    idx, cnt = random_lists(1, H, nb, longest, seed=nb)
+    if group:  # every row sees a key of its own group: its own block's
+        idx = torch.stack([torch.arange(nb), torch.full((nb,), -1)], -1).int().expand(1, H, nb, 2).contiguous().to(DEV)
+        cnt = torch.ones(1, H, nb, dtype=torch.int32, device=DEV)
+    o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, block, group, out_dtype=torch.float32, return_lse=True)
+    dq = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block, group, grad_dtype=torch.float32)[0]
+    for h in range(H):
+        see = list_mask(idx[0, h], cnt[0, h], block, block * nb)
+        if group:
+            i = torch.arange(block * nb, device=DEV) // group
+            see &= i[:, None] == i
+        check_large_mean(dq[0, h], q[0, h], k[0, h], v[0, h], g[0, h], see)
+
+
+@pytest.mark.parametrize("grid,tiles,D", [((3, 9, 17), [(1, 8, 16), (2, 8, 8)], 64), ((5, 6, 12), [(2, 4, 4)], 128),
+                                          ((3, 9, 20), [(1, 4, 16), (1, 8, 8)], 128)])
+def test_short_tiled_lists_gradients_of_keys_with_a_large_mean(grid, tiles, D):
+    """Padding positions hold no key: the mean keys must not count them."""
+    H, S, pg = 2, math.prod(grid), vsa.padded_grid(grid, tiles)
+    positions, block = math.prod(pg), min(128, math.prod(tiles[0]))
+    q, k, v, g = large_mean_inputs(H, S, D)
+    choice = (torch.arange(H) % len(tiles)).int().to(DEV)
+    idx, cnt = random_lists(1, H, positions // block, 4, seed=S)
+    idx[..., 0] = 0  # block 0 holds token 0: no row is without a key
+    o, lse = vsa.block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, out_dtype=torch.float32,
+                                              return_lse=True)
+    dq = vsa.block_sparse_attention_tiled_backward(g, q, k, v, o, lse, grid, tiles, choice, idx, cnt,
+                                                   grad_dtype=torch.float32)[0]
+    for h in range(H):
+        tok = order_of(grid, tiles[int(choice[h])], pg).to(DEV)
+        at = torch.empty(S, dtype=torch.long, device=DEV)
+        at[tok[tok >= 0]] = torch.arange(positions, device=DEV)[tok >= 0]
+        check_large_mean(dq[0, h], q[0, h], k[0, h], v[0, h], g[0, h],
+                         list_mask(idx[0, h], cnt[0, h], block, positions)[at][:, at])
+
+
 @pytest.mark.parametrize("block,nb,longest", [(32, 260, 30), (128, 140, 9)])
 def test_backward_over_many_blocks(block, nb, longest):
     """More than 128 blocks: the lists are turned in global memory.  Sampled against the dense formula."""
