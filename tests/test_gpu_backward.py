@@ -565,6 +565,30 @@ def test_permute_gradients():
     assert torch.equal(torch.autograd.grad(t, z, g)[0], vsa.permute(g, grid, tiles))
 
 
+def test_calls_in_a_row_repeat_bit_for_bit():
+    """Calls right behind one another reuse each other's workspace; a chained kernel that read or wrote too early
+    would mix them up."""
+    cases = []
+    for seed, (nb, longest) in enumerate([(7, 4), (40, 3), (150, 12)]):
+        q, k, v, g = inputs(1, 3, nb * 128, 64, seed=seed)
+        idx, cnt = random_lists(1, 3, nb, longest, seed=seed)
+        table = torch.randn(16, 3, device=DEV)
+
+        def step(q=q, k=k, v=v, g=g, idx=idx, cnt=cnt, table=table):
+            o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, 128, return_lse=True)
+            a = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, 128)
+            o, lse = vsa.window_attention(q, k, v, 300, 20, bias=table, return_lse=True)
+            return (*a, *vsa.window_attention_backward(g, q, k, v, o, lse, 300, 20, bias=table),
+                    *vsa.transpose_block_lists(idx, cnt))
+
+        cases.append((step, step()))
+        torch.cuda.synchronize()
+    for _ in range(15):
+        for got, want in [(step(), want) for step, want in cases]:
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
+
+
 def test_captured_training_step():
     """A recorded forward and backward pass as one graph, replayed over new values."""
     q, k, v, g = inputs(1, 2, 512, 64, seed=21)
