@@ -76,7 +76,6 @@ bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, co
             kb = a.lead + (id - first) - bh * per;
         }
     }
-    grid_release();
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
         for (int s = 0; s < C::NQ; ++s) {
@@ -145,6 +144,9 @@ bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // this CTA has its tensor memory: without a bias's gradient the next kernel is the
+    // caller's, and may allocate some
+    grid_release();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 8) {

@@ -1,0 +1,43 @@
+"""The rules of chained launches (csrc/chain.cuh), checked on the sources: breaking one is a
+hang or a stale read that no run is sure to show."""
+
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_self_b200", "csrc")
+
+
+def kernels():
+    """(file, name, body) of every __global__ function, comments taken out."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for m in re.finditer(r"__global__[^;{]*?(\w+_kernel)\s*\(", text):
+            at = text.index("{", text.index(")", m.end()))
+            depth, end = 1, at + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[end], 0)
+                end += 1
+            yield os.path.basename(path), m.group(1), text[at:end]
+
+
+KERNELS = list(kernels())
+
+
+def test_the_kernels_are_found():
+    names = {k[1] for k in KERNELS}
+    assert {"bwd_dq_kernel", "bwd_dkv_kernel", "attn_pp_kernel", "row_stats_kernel", "list_bits_kernel",
+            "dbias_kernel"} <= names
+
+
+@pytest.mark.parametrize("file,name,body", KERNELS, ids=[f"{f}-{n}" for f, n, _ in KERNELS])
+def test_tensor_memory_is_held_before_the_next_kernel_is_released(file, name, body):
+    """A CTA of the next kernel must not take tensor memory that this kernel still has to allocate."""
+    if "grid_release()" not in body or "tmem_alloc(" not in body:
+        return
+    alloc, release = body.rindex("tmem_alloc("), body.index("grid_release()")
+    assert alloc < release
+    # the allocating warp is one of several: all threads have to know that it is done
+    assert "__syncthreads()" in body[alloc:release]
