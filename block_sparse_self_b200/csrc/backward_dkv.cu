@@ -125,8 +125,8 @@ bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, co
     } else {
         const size_t ls = a.list_per_head ? bh : 0;
         const int32_t *off = a.t_off + ls * (a.nb + 1);
-        const int o0 = __ldg(off + kb);
-        count = __ldg(off + kb + 1) - o0;
+        const int o0 = chain_load(off + kb);
+        count = chain_load(off + kb + 1) - o0;
         list = a.t_rows + ls * a.nb * a.cap + o0;
     }
     if (!head_ok) count = 0;
@@ -135,12 +135,12 @@ bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, co
         if (a.valid) {
             bool any = false;
             for (int u = 0; u < BS / 32; ++u)
-                any = any || __ldg(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + kb * (BS / 32) + u) != 0;
+                any = any || chain_load(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + kb * (BS / 32) + u) != 0;
             if (!any) count = 0;
         }
     }
     const int n = (count + NSUB - 1) / NSUB;
-    auto qblock = [&](int x) { return WINDOW ? q_lo + x : __ldg(list + x); };
+    auto qblock = [&](int x) { return WINDOW ? q_lo + x : chain_load(list + x); };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -166,7 +166,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         if (a.valid) {
             bool any = false;  // a query block wholly in the padding has no row to write
             for (int u = 0; u < BS / 32; ++u)
-                any = any || __ldg(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + qb * (BS / 32) + u) != 0;
+                any = any || chain_load(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + qb * (BS / 32) + u) != 0;
             if (!any) w.count = 0;
         }
     }
@@ -287,8 +287,8 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         const float sl2 = a.scale_log2;
         float nl = -INFINITY, nd = 0.f;
         if (row < BS && p < a.Pw) {
-            nl = __ldg(a.nlse + static_cast<size_t>(bh) * a.Pw + p);
-            nd = __ldg(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
+            nl = chain_load(a.nlse + static_cast<size_t>(bh) * a.Pw + p);
+            nd = chain_load(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
         }
         float row_sum[2] = {0.f, 0.f};
         // CENTER: the row's sum of dX as rounded, the mass of P in this warp's
@@ -339,7 +339,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                             const int c = 64 * hf + 32 * u, x = j * NSUB + c / BS;
                             const int kc = w.at(min(x, w.count - 1)) * BS + c % BS;
                             if (a.group > 0 || a.gstride > 1) see[u] = group_bits(a, p, kc);
-                            if (a.valid) see[u] &= __ldg(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + kc / 32);
+                            if (a.valid) see[u] &= chain_load(a.valid + static_cast<size_t>(bh) * (a.Pw / 32) + kc / 32);
                             if (x >= w.count) see[u] = 0u;  // past the list's end: its last block again
                         }
                     }
@@ -357,7 +357,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                     const int x = WINDOW ? j : min(j * NSUB + 64 * hf / BS + b, w.count - 1);
                     const float *km = a.kmean + (static_cast<size_t>(bh) * a.nt + w.at(x)) * D + CPL * lane;
                     #pragma unroll
-                    for (int e = 0; e < CPL; ++e) mean[b][e] = __ldg(km + e);
+                    for (int e = 0; e < CPL; ++e) mean[b][e] = chain_load(km + e);
                 }
             }
             {

@@ -17,6 +17,10 @@
 //    a CTA of the next kernel must not take it and then wait for this one.  That holds
 //    for the last kernel too: what follows it is the caller's, perhaps a chained launch
 //    of another library that allocates tensor memory.
+//  - what the chain itself wrote is read with chain_load(), never by __ldg() or through
+//    const __restrict__: while a kernel waits, the kernel before may still be writing it,
+//    so it is not read-only for the kernel's lifetime, and a load that may assume so is
+//    not held behind grid_wait().  __ldg() is for the caller's inputs.
 // Without a chained launch before it grid_wait() returns at once.
 // 7 blocks of 128, D = 64, 3 heads: a backward pass every 26.9 us against 38.7 with normal
 // launches (and every tiling's tensor maps as parameters).
@@ -28,6 +32,10 @@ namespace vsa {
 
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// An ordinary load: it stays behind grid_wait(), which clobbers memory.
+template <typename T>
+__device__ __forceinline__ T chain_load(const T *p) { return *p; }
 
 template <typename... P, typename... A>
 inline cudaError_t launch_kernel(bool chained, void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,

@@ -68,7 +68,7 @@ __global__ void expand_kernel(const Borders b, const T *__restrict__ table, int 
 // dtable[b][h]: the partial sums [B, H, per, buckets] over the batch and the
 // key tiles, in a fixed order and in 64 bits.
 template <typename T>
-__global__ void __launch_bounds__(1024) dbias_kernel(const float *__restrict__ part, int B, int H, int per, int buckets,
+__global__ void __launch_bounds__(1024) dbias_kernel(const float *part, int B, int H, int per, int buckets,
                                                      T *__restrict__ dtable) {
     __shared__ double sum[32][33];
     const int b = blockIdx.x * 32 + threadIdx.x, h = blockIdx.y;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(1024) dbias_kernel(const float *__restrict__ p
     if (b < buckets)
         for (int i = threadIdx.y; i < B * per; i += 32) {
             const int n = i / per;
-            s += part[((static_cast<size_t>(n) * H + h) * per + (i - n * per)) * buckets + b];
+            s += chain_load(part + ((static_cast<size_t>(n) * H + h) * per + (i - n * per)) * buckets + b);
         }
     sum[threadIdx.y][threadIdx.x] = s;
     __syncthreads();

@@ -21,6 +21,7 @@
 
 #include <stdint.h>
 
+#include "chain.cuh"
 #include "common.cuh"
 
 namespace vsa {
@@ -29,7 +30,7 @@ constexpr int kMaxBuckets = 256;
 
 // bm points at offset 0; offsets beyond R share the bucket of R on their side.
 __device__ __forceinline__ int bias_bucket(const uint8_t *bm, int R, int o) {
-    return __ldg(bm + min(max(o, -R), R));
+    return chain_load(bm + min(max(o, -R), R));
 }
 
 enum : int { BIAS_ONE = 0, BIAS_TWO = 1, BIAS_MORE = 2 };
@@ -61,7 +62,7 @@ __device__ __forceinline__ float bias_at(float lo, float hi, int i, int lane) {
 
 // The head's values by bucket (log2e already in them) to shared memory.
 __device__ __forceinline__ void bias_table(float *smem, const float *tab, int head, int buckets, int thread, int threads) {
-    for (int b = thread; b < buckets; b += threads) smem[b] = __ldg(tab + static_cast<size_t>(head) * buckets + b);
+    for (int b = thread; b < buckets; b += threads) smem[b] = chain_load(tab + static_cast<size_t>(head) * buckets + b);
 }
 
 }  // namespace vsa

@@ -83,8 +83,7 @@ __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t *__restric
 }
 
 // One CTA per list: offsets[k] = entries of the key blocks before k.
-__global__ void __launch_bounds__(1024) list_offsets_kernel(const uint32_t *__restrict__ bits, int nb, int cols,
-                                                            int32_t *__restrict__ offsets) {
+__global__ void __launch_bounds__(1024) list_offsets_kernel(const uint32_t *bits, int nb, int cols, int32_t *offsets) {
     __shared__ int warp_sum[32];
     const size_t list = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(1024) list_offsets_kernel(const uint32_t *__re
         int c = 0;
         if (k < nb) {
             #pragma unroll 8
-            for (int i = 0; i < cols; ++i) c += __popc(__ldg(b + static_cast<size_t>(i) * nb + k));
+            for (int i = 0; i < cols; ++i) c += __popc(chain_load(b + static_cast<size_t>(i) * nb + k));
         }
         int s = c;
         #pragma unroll
@@ -127,9 +126,8 @@ __global__ void __launch_bounds__(1024) list_offsets_kernel(const uint32_t *__re
 }
 
 // One warp per (key block, list); also -1 behind the last entry when asked.
-__global__ void __launch_bounds__(256) list_rows_kernel(const uint32_t *__restrict__ bits,
-                                                        const int32_t *__restrict__ offsets, int nb, int cols, int cap,
-                                                        int fill, int32_t *__restrict__ rows) {
+__global__ void __launch_bounds__(256) list_rows_kernel(const uint32_t *bits, const int32_t *offsets, int nb, int cols,
+                                                        int cap, int fill, int32_t *rows) {
     const int key = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const size_t list = blockIdx.y;
     grid_release();
@@ -137,10 +135,10 @@ __global__ void __launch_bounds__(256) list_rows_kernel(const uint32_t *__restri
     if (key >= nb) return;
     const uint32_t *b = bits + list * cols * nb + key;
     int32_t *out = rows + list * nb * cap;
-    int at = __ldg(offsets + list * (nb + 1) + key);
+    int at = chain_load(offsets + list * (nb + 1) + key);
     for (int c0 = 0; c0 < cols; c0 += 32) {
         const int c = c0 + lane;
-        uint32_t w = c < cols ? __ldg(b + static_cast<size_t>(c) * nb) : 0u;
+        uint32_t w = c < cols ? chain_load(b + static_cast<size_t>(c) * nb) : 0u;
         int s = __popc(w);
         const int mine = s;
         #pragma unroll
@@ -152,7 +150,7 @@ __global__ void __launch_bounds__(256) list_rows_kernel(const uint32_t *__restri
         at += __shfl_sync(0xffffffffu, s, 31);
     }
     if (fill) {
-        const int total = __ldg(offsets + list * (nb + 1) + nb);
+        const int total = chain_load(offsets + list * (nb + 1) + nb);
         for (int e = key * cap + lane; e < (key + 1) * cap; e += 32)
             if (e >= total) out[e] = -1;
     }

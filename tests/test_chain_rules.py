@@ -41,3 +41,19 @@ def test_tensor_memory_is_held_before_the_next_kernel_is_released(file, name, bo
     assert alloc < release
     # the allocating warp is one of several: all threads have to know that it is done
     assert "__syncthreads()" in body[alloc:release]
+
+
+# what the kernels of a chain hand to one another, by the names that the readers use
+HANDED_ON = r"nlse|ndelta|valid|km|kmean|off|offsets|bits|part|tab|bm|t_off|t_rows"
+
+
+@pytest.mark.parametrize("file", ["attention_pp.cu", "backward.cu", "backward_dkv.cu", "backward_dq.cu",
+                                  "relative_bias.cu", "relative_bias.cuh", "transpose_lists.cu"])
+def test_what_the_chain_wrote_is_not_read_as_constant(file):
+    """A read-only load may be moved across the wait for the kernel that writes the value."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, file)).read())
+    for m in re.finditer(r"__ldg\(([^;]*);", text):
+        assert not re.search(r"\b(%s)\b" % HANDED_ON, m.group(1)), m.group(0)
+    assert not re.search(r"const[^,()]*__restrict__ (%s)\b" % HANDED_ON, text)
+    if file == "backward_dkv.cu":  # the transposed lists
+        assert "__ldg(list" not in text
