@@ -496,12 +496,30 @@ def _lists_arg(idx, cnt):
 
 
 def _check_lists(idx, cnt, B, H, nb):
-    """The shapes that the training calls rely on: [B, H, nb, cap] and [B, H, nb], or [nb, cap] and [nb]."""
-    _lists_arg(idx, cnt)
-    want = (B, H, nb) if idx.dim() == 4 else (nb,)
-    if tuple(idx.shape[:-1]) != want or tuple(cnt.shape) != want:
+    """Lists of another grid, block size or number of heads would be read past their end: idx is [B, H, nb, cap],
+    or one list for all heads (nb rows in all), and cnt has an entry for each of its rows."""
+    rows = idx.shape[:-1]
+    if (tuple(rows) != (B, H, nb) if idx.dim() == 4 else idx.dim() < 2 or rows.numel() != nb) or (
+            cnt.shape != rows and (cnt.dim() != 1 or cnt.numel() != rows.numel())):
         raise ValueError(f"idx and cnt must be [B, H, nb, cap] and [B, H, nb], or [nb, cap] and [nb], with nb = {nb}; "
                          f"got {tuple(idx.shape)} and {tuple(cnt.shape)}")
+
+
+def _check_block_lists(idx, cnt, B, H, S, block):
+    """_check_lists for blocks of a sequence in tile-contiguous order."""
+    if block not in (32, 64, 128) or S % block:
+        raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
+    _check_lists(idx, cnt, B, H, S // block)
+
+
+def _check_tiled_lists(idx, cnt, B, H, grid, tiles):
+    """_check_lists for blocks of the padded grid; the number of its positions, and the block."""
+    positions, volume = _grid_tokens(padded_grid(grid, tiles)), math.prod(int(x) for x in tiles[0])
+    block = min(128, volume)
+    if volume not in (32, 64) and volume % 128:
+        raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {volume}")
+    _check_lists(idx, cnt, B, H, positions // block)
+    return positions, block
 
 
 def _same_device(ref, **tensors):
@@ -586,6 +604,7 @@ class _BlockSparse(torch.autograd.Function):
 
 def _lists_forward(qb, kb, vb, odt, remainder, idx, cnt, _, block, group_size, scale):
     B, H, S, D = qb.shape
+    _check_block_lists(idx, cnt, B, H, S, block)
     _same_device(qb, k=kb, v=vb, idx=idx, cnt=cnt)
     o = _like(qb, odt)
     lse, o_lo = _saved_outputs(o, remainder)
@@ -599,9 +618,8 @@ def _lists_forward(qb, kb, vb, odt, remainder, idx, cnt, _, block, group_size, s
 
 def _lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, _, block, group_size, scale):
     B, H, S, D = qb.shape
-    if block not in (32, 64, 128) or S % block:
-        raise ValueError(f"block must be 32, 64 or 128 and divide S ({S}), got {block}")
-    _check_lists(idx, cnt, B, H, S // block)
+    _lists_arg(idx, cnt)
+    _check_block_lists(idx, cnt, B, H, S, block)
     _same_device(qb, idx=idx, cnt=cnt)
     cap, per_head = idx.shape[-1], 1 if idx.dim() == 4 else 0
     dq, dk, dv = _like(qb, gdt), _like(qb, gdt), _like(qb, gdt)
@@ -638,6 +656,7 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     if return_lse or return_remainder:
         return _saved(*_lists_forward(qb, kb, vb, odt, return_remainder, idx, cnt, None, *rest), return_lse,
                       return_remainder)
+    _check_block_lists(idx, cnt, B, H, S, int(block))
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     cap = idx.shape[-1]
     per_head = idx.dim() == 4
@@ -694,14 +713,12 @@ def centroid_compensated_attention(q, k, v, idx, cnt, block: int = 128, scale: O
                          f"v={tuple(v.shape)}")
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-    _cuda(idx, "idx")
-    _cuda(cnt, "cnt")
-    if idx.dtype != torch.int32 or cnt.dtype != torch.int32:
-        raise ValueError("idx and cnt must be int32")
+    _lists_arg(idx, cnt)
     oc = BF16 if odt == torch.bfloat16 else F32
     need = lib().vsa_centroid_compensated_attention_workspace_size(B, H, S, D, oc)
     if need == 0:
         raise ValueError(f"no workspace size for B={B}, H={H}, S={S}, D={D} (S must be a multiple of 128, D 64 or 128)")
+    _check_lists(idx, cnt, B, H, S // 128)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     _check(lib().vsa_centroid_compensated_attention(
@@ -721,14 +738,12 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
                          f"v={tuple(v.shape)}")
     odt = _out_dtype(out_dtype, q)
     qb, kb, vb = _bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v")
-    _cuda(idx, "idx")
-    _cuda(cnt, "cnt")
-    if idx.dtype != torch.int32 or cnt.dtype != torch.int32:
-        raise ValueError("idx and cnt must be int32")
+    _lists_arg(idx, cnt)
     oc = BF16 if odt == torch.bfloat16 else F32
     need = lib().vsa_centroid_compensated_attention_workspace_size(B, H, S, D, oc)
     if need == 0:
         raise ValueError(f"no workspace size for B={B}, H={H}, S={S}, D={D} (S must be a multiple of 128, D 64 or 128)")
+    _check_lists(idx, cnt, B, H, S // 128)
     arr, n = _tiles_arg(tiles)
     ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
@@ -741,6 +756,7 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
 
 def _tiled_lists_forward(qb, kb, vb, odt, remainder, idx, cnt, choice, grid, tiles, group_stride, scale):
     B, H, S, D = qb.shape
+    _check_tiled_lists(idx, cnt, B, H, grid, tiles)
     _same_device(qb, k=kb, v=vb, idx=idx, cnt=cnt, choice=choice)
     arr, n = _tiles_arg(tiles)
     o = _like(qb, odt)
@@ -756,11 +772,8 @@ def _tiled_lists_forward(qb, kb, vb, odt, remainder, idx, cnt, choice, grid, til
 def _tiled_lists_backward(gb, qb, kb, vb, o, lse, o_lo, gdt, idx, cnt, choice, grid, tiles, group_stride, scale):
     B, H, S, D = qb.shape
     arr, n = _tiles_arg(tiles)
-    positions = _grid_tokens(padded_grid(grid, tiles))
-    block = min(128, math.prod(int(x) for x in tiles[0]))
-    if block not in (32, 64, 128) or positions % block:
-        raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {math.prod(tiles[0])}")
-    _check_lists(idx, cnt, B, H, positions // block)
+    _lists_arg(idx, cnt)
+    positions, block = _check_tiled_lists(idx, cnt, B, H, grid, tiles)
     _same_device(qb, idx=idx, cnt=cnt, choice=choice)
     cap, per_head = idx.shape[-1], 1 if idx.dim() == 4 else 0
     dq, dk, dv = _like(qb, gdt), _like(qb, gdt), _like(qb, gdt)
@@ -795,6 +808,7 @@ def block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale: 
     if return_lse or return_remainder:
         return _saved(*_tiled_lists_forward(qb, kb, vb, odt, return_remainder, idx, cnt, choice, *rest), return_lse,
                       return_remainder)
+    _check_tiled_lists(idx, cnt, B, H, grid, tiles)
     arr, n = _tiles_arg(tiles)
     o = torch.empty(B, H, S, D, dtype=odt, device=q.device)
     _check(lib().vsa_block_sparse_attention_tiled(

@@ -1,0 +1,112 @@
+"""Argument checks of the Python binding, on the CPU: tensors stand in for CUDA tensors and a
+launch that is reached is recorded in place of being made."""
+
+import math
+
+import pytest
+import torch
+
+import block_sparse_self_b200 as vsa
+
+
+class Launched(Exception):
+    pass
+
+
+class Recorder:
+    """libvsa with every call that would launch something replaced by the exception above."""
+
+    def __init__(self, real):
+        self.real = real
+
+    def __getattr__(self, name):
+        if name == "vsa_padded_grid" or name.endswith("workspace_size") or name == "vsa_last_error":
+            return getattr(self.real, name)
+
+        def launch(*args):
+            raise Launched(name)
+        return launch
+
+
+@pytest.fixture
+def host(monkeypatch):
+    real = vsa.lib()
+    monkeypatch.setattr(vsa, "_cuda", lambda t, name: t)
+    monkeypatch.setattr(vsa, "lib", lambda: Recorder(real))
+    monkeypatch.setattr(vsa, "_stream", lambda device=None: 0)
+    monkeypatch.setattr(vsa, "_on", lambda t: vsa._NO_GUARD)
+
+
+def qkv(B, H, S, D=64, **kw):
+    return [torch.zeros(B, H, S, D, dtype=torch.bfloat16, **kw) for _ in range(3)]
+
+
+def lists(*lead, cap=2):
+    return torch.zeros(*lead, cap, dtype=torch.int32), torch.ones(*lead, dtype=torch.int32)
+
+
+B, H, NB = 2, 3, 4
+GRID, TILES = (4, 8, 16), [(1, 8, 16)]
+BAD = {
+    "too few blocks": lists(B, H, NB - 1),
+    "too many blocks": lists(B, H, NB + 1),
+    "too few heads": lists(B, H - 1, NB),
+    "batch and heads exchanged": lists(H, B, NB),
+    "a list per head without the batch": lists(H, NB),
+    "a short shared list": lists(NB - 1),
+    "a short cnt": (lists(B, H, NB)[0], torch.ones(B, H, NB - 1, dtype=torch.int32)),
+    "a cnt of one head": (lists(B, H, NB)[0], torch.ones(NB, dtype=torch.int32)),
+    "cnt in another order": (lists(B, H, NB)[0], torch.ones(B, NB, H, dtype=torch.int32)),
+    "one row": (torch.zeros(NB, dtype=torch.int32), torch.ones(NB, dtype=torch.int32)),
+}
+GOOD = {"per head": lists(B, H, NB), "shared": lists(NB), "shared, 3-D": lists(1, NB),
+        "flat counts": (lists(B, H, NB)[0], torch.ones(B * H * NB, dtype=torch.int32))}
+
+
+def calls(q, k, v):
+    lse, x = torch.zeros(B, H, q.shape[2]), q
+    leaf = q.clone().requires_grad_()
+    yield "plain", lambda i, c: vsa.block_sparse_attention(q, k, v, i, c, 128)
+    yield "lse", lambda i, c: vsa.block_sparse_attention(q, k, v, i, c, 128, return_lse=True)
+    yield "autograd", lambda i, c: vsa.block_sparse_attention(leaf, k, v, i, c, 128)
+    yield "backward", lambda i, c: vsa.block_sparse_attention_backward(x, q, k, v, x, lse, i, c, 128)
+    yield "tiled", lambda i, c: vsa.block_sparse_attention_tiled(q, k, v, GRID, TILES, None, i, c)
+    yield "tiled lse", lambda i, c: vsa.block_sparse_attention_tiled(q, k, v, GRID, TILES, None, i, c, return_lse=True)
+    yield "tiled autograd", lambda i, c: vsa.block_sparse_attention_tiled(leaf, k, v, GRID, TILES, None, i, c)
+    yield "tiled backward", lambda i, c: vsa.block_sparse_attention_tiled_backward(x, q, k, v, x, lse, GRID, TILES, None,
+                                                                                   i, c)
+    yield "compensated", lambda i, c: vsa.centroid_compensated_attention(q, k, v, i, c)
+    yield "compensated tiled", lambda i, c: vsa.centroid_compensated_attention_tiled(q, k, v, GRID, TILES, None, i, c)
+
+
+@pytest.mark.parametrize("call", [name for name, _ in calls(*qkv(B, H, 512))])
+def test_lists_of_another_shape_are_refused(host, call):
+    """Every list call indexes nb rows per head of idx and cnt: fewer would be read past their end."""
+    q, k, v = qkv(B, H, math.prod(GRID))
+    run = dict(calls(q, k, v))[call]
+    for what, (idx, cnt) in BAD.items():
+        with pytest.raises(ValueError, match="idx and cnt"):
+            run(idx, cnt)
+            pytest.fail(what)
+    for what, (idx, cnt) in GOOD.items():
+        with pytest.raises(Launched):
+            run(idx, cnt)
+
+
+def test_blocks_of_the_padded_grid_are_counted(host):
+    """A grid that the tiles do not divide has the lists of its padded grid."""
+    grid = (3, 7, 20)                       # padded to (3, 8, 32): 6 blocks
+    q, k, v = qkv(1, 1, math.prod(grid))
+    for lse in (False, True):
+        with pytest.raises(ValueError, match="nb = 6"):
+            vsa.block_sparse_attention_tiled(q, k, v, grid, TILES, None, *lists(1, 1, 4), return_lse=lse)
+        with pytest.raises(Launched):
+            vsa.block_sparse_attention_tiled(q, k, v, grid, TILES, None, *lists(1, 1, 6), return_lse=lse)
+
+
+@pytest.mark.parametrize("block", [0, -128, 48, 96, 256])
+def test_block_sizes_that_are_refused(host, block):
+    q, k, v = qkv(1, 1, 768)
+    for lse in (False, True):
+        with pytest.raises(ValueError, match="block"):
+            vsa.block_sparse_attention(q, k, v, *lists(1, 1, 6), block, return_lse=lse)
