@@ -1025,7 +1025,8 @@ def spade_attention(q, k, v, grid, tiles, budget: Optional[float] = None, topk: 
     tiled=True runs the permutation inside the summaries and attention kernels
     (no permuted copies; blocks of 32, 64 or 128 tokens, see tiled_supported); tiled=False
     runs the explicit permute / unpermute steps; None picks tiled when it is
-    supported.  Both give identical results.  In tiled mode the permuted
+    supported.  Both give identical results, in out_dtype; without one, tiled
+    mode gives bfloat16 and the other q's type.  In tiled mode the permuted
     tensors in the intermediates are computed afterwards, for inspection only.
     """
     tiles = [tuple(t) for t in tiles]
@@ -1057,10 +1058,11 @@ def spade_attention(q, k, v, grid, tiles, budget: Optional[float] = None, topk: 
         kmax, kmin = block_summaries_tiled(k, grid, tiles, choice, block)
         scores = block_scores(qmax, qmin, kmax, kmin)
         idx, cnt = _select_blocks(scores, kk, n_sink_blocks, diag_halfwidth, top_p, top_p_scale, D)
+        odt = torch.bfloat16 if out_dtype is None else out_dtype
         if compensate:
-            o = centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, out_dtype)
+            o = centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, odt)
         else:
-            o = block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, out_dtype)
+            o = block_sparse_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt, scale, odt)
         if return_intermediates:
             qp, kp, vp, op = (permute(x, grid, tiles, choice) for x in (q, k, v, o))
     else:

@@ -110,3 +110,23 @@ def test_block_sizes_that_are_refused(host, block):
     for lse in (False, True):
         with pytest.raises(ValueError, match="block"):
             vsa.block_sparse_attention(q, k, v, *lists(1, 1, 6), block, return_lse=lse)
+
+
+@pytest.mark.parametrize("compensate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tiled_spade_attention_gives_bfloat16_unless_told(host, monkeypatch, dtype, compensate):
+    """Inputs in fp32 are rounded to bf16 on the way in; the output type is bf16 unless out_dtype says otherwise."""
+    asked = []
+
+    def attention(q, k, v, grid, tiles, choice, idx, cnt, scale, out_dtype):
+        asked.append(vsa._out_dtype(out_dtype, q))
+        return q
+
+    for name in ("block_summaries_tiled", "block_scores", "_select_blocks"):
+        monkeypatch.setattr(vsa, name, lambda *a: (None, None))
+    monkeypatch.setattr(vsa, "block_sparse_attention_tiled", attention)
+    monkeypatch.setattr(vsa, "centroid_compensated_attention_tiled", attention)
+    q, k, v = (x.to(dtype) for x in qkv(1, 1, math.prod(GRID)))
+    vsa.spade_attention(q, k, v, GRID, TILES, topk=1, compensate=compensate)
+    vsa.spade_attention(q, k, v, GRID, TILES, topk=1, compensate=compensate, out_dtype=torch.float32)
+    assert asked == [torch.bfloat16, torch.float32]
