@@ -701,12 +701,30 @@ def transpose_block_lists(idx, cnt):
     return offsets, rows
 
 
+class _NoBackward(torch.autograd.Function):
+    """A call that has no backward pass: its result belongs to the graph, so that a gradient which would be
+    missing is an error and not a silent zero."""
+
+    @staticmethod
+    def forward(ctx, call, name, *tensors):
+        ctx.name = name
+        return call(*tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise NotImplementedError(f"{ctx.name} has no backward pass; call it under torch.no_grad(), or detach its result")
+
+
 def centroid_compensated_attention(q, k, v, idx, cnt, block: int = 128, scale: Optional[float] = None,
                                    out_dtype=None) -> torch.Tensor:
     """Block-sparse attention (tile-contiguous order, 128-token blocks) in which
     every key block a query block's list skips still takes part, as one key:
     the block's mean key, with its mean value, weighted by its key count (see
-    include/vsa.h for the reading of the pages' call)."""
+    include/vsa.h for the reading of the pages' call).  It has no backward
+    pass: going back through its result raises NotImplementedError."""
+    if _wants_grad(q, k, v):
+        return _NoBackward.apply(lambda *x: centroid_compensated_attention(*x, idx, cnt, block, scale, out_dtype),
+                                 "compensated attention", q, k, v)
     B, H, S, D = _bhsd(q, "q")
     if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
         raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
@@ -731,7 +749,12 @@ def centroid_compensated_attention_tiled(q, k, v, grid, tiles, choice, idx, cnt,
                                          out_dtype=None) -> torch.Tensor:
     """unpermute(centroid_compensated_attention(permute(q), permute(k), permute(v), idx, cnt)) with no
     permuted copies: q, k, v and the result in T-major order, each head's 128-token blocks those of
-    tiles[choice[b, h]] (tiling 0 without a choice); the tiles must divide the grid."""
+    tiles[choice[b, h]] (tiling 0 without a choice); the tiles must divide the grid.  No backward pass,
+    as there."""
+    if _wants_grad(q, k, v):
+        return _NoBackward.apply(lambda *x: centroid_compensated_attention_tiled(*x, grid, tiles, choice, idx, cnt,
+                                                                                 scale, out_dtype),
+                                 "compensated attention", q, k, v)
     B, H, S, D = _bhsd(q, "q")
     if tuple(k.shape) != (B, H, S, D) or tuple(v.shape) != (B, H, S, D):
         raise ValueError(f"q/k/v shapes must match exactly; got q={tuple(q.shape)}, k={tuple(k.shape)}, "
@@ -1019,8 +1042,8 @@ def spade_attention(q, k, v, grid, tiles, budget: Optional[float] = None, topk: 
     1/sqrt(D); budget and topk are then unused.
 
     Differentiable in q, k and v, the tiling choice and the lists being
-    constants of the backward pass; with compensate=True the result carries no
-    gradient.
+    constants of the backward pass; with compensate=True there is no backward
+    pass, and going back through the result raises NotImplementedError.
 
     tiled=True runs the permutation inside the summaries and attention kernels
     (no permuted copies; blocks of 32, 64 or 128 tokens, see tiled_supported); tiled=False

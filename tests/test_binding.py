@@ -130,3 +130,29 @@ def test_tiled_spade_attention_gives_bfloat16_unless_told(host, monkeypatch, dty
     vsa.spade_attention(q, k, v, GRID, TILES, topk=1, compensate=compensate)
     vsa.spade_attention(q, k, v, GRID, TILES, topk=1, compensate=compensate, out_dtype=torch.float32)
     assert asked == [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("tiled", [False, True])
+def test_going_back_through_compensated_attention_is_an_error(host, monkeypatch, tiled):
+    """Beside other terms of a loss a result without a graph would train with a gradient missing."""
+    class Fills(Recorder):
+        def __getattr__(self, name):
+            if name in ("vsa_centroid_compensated_attention", "vsa_centroid_compensated_attention_tiled"):
+                return lambda *args: vsa.OK
+            return super().__getattr__(name)
+
+    real = vsa.lib().real
+    monkeypatch.setattr(vsa, "lib", lambda: Fills(real))
+    q, k, v = qkv(B, H, math.prod(GRID))
+    leaf = q.clone().requires_grad_()
+    tail = (GRID, TILES, None, *lists(B, H, NB)) if tiled else lists(B, H, NB)
+    call = vsa.centroid_compensated_attention_tiled if tiled else vsa.centroid_compensated_attention
+    o = call(leaf, k, v, *tail)
+    with pytest.raises(NotImplementedError, match="compensated"):
+        (o.float().sum() + leaf.float().sum()).backward()
+    # without recording, and for inputs that need no gradient, nothing changes
+    with torch.no_grad():
+        assert not call(leaf, k, v, *tail).requires_grad
+    assert not call(q, k, v, *tail).requires_grad
+    with pytest.raises(ValueError, match="idx and cnt"):
+        call(leaf, k, v, *(GRID, TILES, None) if tiled else (), *lists(B, H, NB - 1))
