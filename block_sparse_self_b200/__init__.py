@@ -573,6 +573,12 @@ def _saved(o, lse, o_lo, return_lse, return_remainder):
     return (o, lse) if return_lse else o
 
 
+def _refuse_saved(grads):
+    """lse and the remainder are there for the backward functions; a gradient that comes back for one would be lost."""
+    if any(g is not None for g in grads):
+        raise NotImplementedError("gradients of lse and of the remainder are not computed; detach them")
+
+
 def _grads_as(grads, dtypes):
     return tuple(g if g.dtype == t else g.to(t) for g, t in zip(grads, dtypes))
 
@@ -587,13 +593,13 @@ class _BlockSparse(torch.autograd.Function):
         o, lse, o_lo = fwd(qb, kb, vb, _out_dtype(out_dtype, q), True, idx, cnt, choice, *rest)
         ctx.bwd, ctx.rest, ctx.dtypes = bwd, rest, (q.dtype, k.dtype, v.dtype)
         ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, idx, cnt, choice)
-        ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
         return o, lse, o_lo
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, do, *_):
+    def backward(ctx, do, *saved):
+        _refuse_saved(saved)
         if do is None:
             return (None,) * 10
         qb, kb, vb, o, lse, o_lo, idx, cnt, choice = ctx.saved_tensors
@@ -644,7 +650,9 @@ def block_sparse_attention(q, k, v, idx, cnt, block: int, group_size: int = 0, s
     exact as with an fp32 output.  With either, and where gradients are
     recorded, blocks of 32 and 64 tokens run on a kernel of their own whose
     output is rounded differently.
-    Differentiable in q, k and v; the lists are constants of the backward pass."""
+    Differentiable in q, k and v; the lists are constants of the backward pass.
+    Only the output is: going back through lse or the remainder raises
+    NotImplementedError."""
     B, H, S, D = _qkv_shape(q, k, v)
     odt = _out_dtype(out_dtype, q)
     _lists_arg(idx, cnt)
@@ -886,13 +894,13 @@ class _Window(torch.autograd.Function):
         o, lse, o_lo = _window_forward(qb, kb, vb, out_dtype, True, True, bias, *args)
         ctx.args, ctx.dtypes = args, (q.dtype, k.dtype, v.dtype)
         ctx.save_for_backward(qb, kb, vb, o, lse, o_lo, bias)
-        ctx.mark_non_differentiable(*(t for t in (lse, o_lo) if t is not None))
         ctx.set_materialize_grads(False)
         return o, lse, o_lo
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, do, *_):
+    def backward(ctx, do, *saved):
+        _refuse_saved(saved)
         if do is None:
             return (None,) * 6
         qb, kb, vb, o, lse, o_lo, bias = ctx.saved_tensors

@@ -156,3 +156,29 @@ def test_going_back_through_compensated_attention_is_an_error(host, monkeypatch,
     assert not call(q, k, v, *tail).requires_grad
     with pytest.raises(ValueError, match="idx and cnt"):
         call(leaf, k, v, *(GRID, TILES, None) if tiled else (), *lists(B, H, NB - 1))
+
+
+@pytest.mark.parametrize("call", ["lists", "tiled", "window"])
+@pytest.mark.parametrize("what", [1, 2])
+def test_going_back_through_lse_or_the_remainder_is_an_error(host, monkeypatch, call, what):
+    """A term of the loss that uses them would otherwise train with its gradient missing."""
+    class Fills(Recorder):
+        def __getattr__(self, name):
+            if name in ("vsa_block_sparse_attention_lse", "vsa_block_sparse_attention_tiled_lse",
+                        "vsa_window_attention_lse"):
+                return lambda *args: vsa.OK
+            return super().__getattr__(name)
+
+    real = vsa.lib().real
+    monkeypatch.setattr(vsa, "lib", lambda: Fills(real))
+    q, k, v = qkv(B, H, math.prod(GRID))
+    leaf = q.clone().requires_grad_()
+    kw = dict(return_lse=True, return_remainder=True)
+    if call == "lists":
+        out = vsa.block_sparse_attention(leaf, k, v, *lists(B, H, NB), 128, **kw)
+    elif call == "tiled":
+        out = vsa.block_sparse_attention_tiled(leaf, k, v, GRID, TILES, None, *lists(B, H, NB), **kw)
+    else:
+        out = vsa.window_attention(leaf, k, v, 64, **kw)
+    with pytest.raises(NotImplementedError, match="lse"):
+        (out[0].float().sum() + out[what].float().sum() + leaf.float().sum()).backward()
