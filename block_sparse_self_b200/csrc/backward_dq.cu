@@ -466,7 +466,9 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         const int r = rows_live && row < BS && head_ok ? bwd_row_of<TILED>(p, a, tc) : -1;
         const size_t at = (static_cast<size_t>(bh) * a.S_out + max(r, 0)) * D;
         bool have = ok && n > 0;
-        if (have && !__all_sync(0xffffffffu, mbar_wait(dq_done, (n - 1) & 1, abort_flag))) {
+        // mma_done and not dq_done: that one has a phase per tile, and its parity alone does
+        // not tell the last phase from the one before the last but one
+        if (have && !__all_sync(0xffffffffu, mbar_wait(mma_done, 0, abort_flag))) {
             have = false;
             if (!*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
         }

@@ -57,3 +57,11 @@ def test_what_the_chain_wrote_is_not_read_as_constant(file):
     assert not re.search(r"const[^,()]*__restrict__ (%s)\b" % HANDED_ON, text)
     if file == "backward_dkv.cu":  # the transposed lists
         assert "__ldg(list" not in text
+
+
+def test_the_dq_epilogue_waits_for_a_barrier_of_one_phase():
+    """dq_done completes a phase per tile; a thread that has not followed every phase must not wait on its parity."""
+    (body,) = (b for f, n, b in KERNELS if n == "bwd_dq_kernel")
+    work = body[body.index("row_sum"):]     # the element-wise warps' part
+    assert "mbar_wait(mma_done, 0" in work and "mbar_wait(dq_done" not in work
+    assert body.count("umma_commit(mma_done)") == 1
