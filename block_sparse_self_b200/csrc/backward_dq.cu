@@ -487,11 +487,14 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         if (have) {
             if (rows_live) {
                 tc_fence_after();
-                [[maybe_unused]] float used = 0.f;
+                // the center first, then times the row's sum: a mass as small as fp32 has (all
+                // weight on columns that do not count for it) would take the sum to infinity
+                [[maybe_unused]] float used = 0.f, inv = 0.f;
                 [[maybe_unused]] const float *c0 = sMean + wq * (D + 1), *c1 = sMean + (wq + 4) * (D + 1);
                 if constexpr (CENTER) {
                     const float total = c0[D] + c1[D];
-                    used = total > 0.f ? (sUsed[row] + sUsed[128 + row]) / total : 0.f;
+                    inv = total > 0.f ? 1.f / total : 0.f;
+                    used = sUsed[row] + sUsed[128 + row];
                 }
                 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
@@ -502,7 +505,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                     if constexpr (CENTER) {
                         #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            x[e] = __float_as_uint(fmaf(-used, c0[col + e] + c1[col + e], __uint_as_float(x[e])));
+                            x[e] = __float_as_uint(fmaf(-used, (c0[col + e] + c1[col + e]) * inv, __uint_as_float(x[e])));
                     }
                     if (r >= 0) bwd_store32(x, a.scale, a.d0, a.out_f32, at + col);
                 }
