@@ -952,7 +952,8 @@ def window_attention(q, k, v, window: int, sink: int = 0, scale: Optional[float]
     bias ([num_buckets, H], float32 or bfloat16) is a learned relative position
     bias: bias[bucket(j - i), h] is added to the scaled logit of query i and key
     j of head h, with the buckets of relative_position_buckets(num_buckets,
-    max_distance).  return_lse and return_remainder as for block_sparse_attention.
+    max_distance).  An entry of -inf or the type's lowest value masks its bucket;
+    entries of any other size count, lse then as include/vsa.h says.  return_lse and return_remainder as for block_sparse_attention.
     Differentiable in q, k, v and bias."""
     B, H, S, D = _qkv_shape(q, k, v)
     if chunk_size is not None and int(chunk_size) < 1:

@@ -11,6 +11,19 @@
 // The attention kernels read bucket(r) as a byte, for |r| <= R = min(far, S)
 // (larger offsets fall into the last bucket of their side), and each head's
 // values tab[h][b] = log2(e) table[b][h].
+//
+// Entries of a size at which fp32 no longer holds a logit beside them (a mask by
+// -1e9) are moved closer.  The softmax of a row does not change when all its logits
+// move together, and not either when a distance between them that leaves the lower
+// one no weight becomes another such distance.  So where a head's entries, in order,
+// leave a gap of more than 2839, the gap becomes 2839, and a head whose largest entry
+// is beyond +-2839 moves to 0 as a whole: in the table's own units, where distances of
+// close entries are exact.  A row that sees only entries below such a gap then has
+// logits of about 2^12 (2839 log2 e), whose roundings move its probabilities by 2^-12
+// of themselves, where at 1e9 nothing was left of them: P recomputed from lse summed
+// to anything between 0.2 and 5200.
+// Every row sees its own key, so nothing below that key's bucket needs an order of
+// its own: all that is more than the gap below it is put at the gap.
 #include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -53,16 +66,81 @@ __global__ void buckets_kernel(const Borders b, int far, int32_t *__restrict__ o
     if (x <= 2 * far) out[x] = bucket_of(x - far, b);
 }
 
-template <typename T>
-__global__ void expand_kernel(const Borders b, const T *__restrict__ table, int H, int buckets, int R,
-                              float *__restrict__ tab, uint8_t *__restrict__ bm) {
-    const int x = blockIdx.x * 256 + threadIdx.x;
-    grid_release();
-    if (x <= 2 * R) bm[x] = static_cast<uint8_t>(bucket_of(x - R, b));
-    if (x < H * buckets) {
-        const int h = x / buckets, k = x - h * buckets;
-        tab[x] = static_cast<float>(table[static_cast<size_t>(k) * H + h]) * 1.4426950408889634f;
+constexpr int kMost = 256;           // buckets
+constexpr float kGap = 2839.f;       // the most that is left of a gap, and of the largest entry
+constexpr float kMask = -0x1p127f;   // entries below it mask (times log2 e they would leave fp32)
+
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// s[0 .. n): one head's entries, s[0] that of a row's own key.  Where
+// this thread's entry goes (see above); called by all threads of the CTA.
+__device__ float closer(const float *s, int n, int k, float top, float low, float *sorted, float *place) {
+    const float mine = s[k];
+    const float self = is_finite(s[0]) ? s[0] : low;
+    const bool counts = k < n && is_finite(mine) && mine >= self;
+    int rank = 0, m = 0;
+    for (int j = 0; j < n; ++j) {
+        const float x = s[j];
+        if (!is_finite(x) || x < self) continue;
+        ++m;
+        if (x > mine || (x == mine && j < k)) ++rank;
     }
+    if (counts) sorted[rank] = mine;  // descending
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // entries of a run without a wide gap keep their distances to its first
+        float first = top, at = fabsf(top) <= kGap ? top : 0.f;
+        for (int j = 0; j < m; ++j) {
+            if (j > 0 && sorted[j - 1] - sorted[j] > kGap) {
+                at = place[j - 1] - kGap;
+                first = sorted[j];
+            }
+            place[j] = at == first ? sorted[j] : at - (first - sorted[j]);
+        }
+    }
+    __syncthreads();
+    if (counts) return place[rank];
+    if (!is_finite(mine)) return mine;
+    const float at = place[m - 1];
+    return at == self ? fmaxf(mine, self - kGap) : at - fminf(self - mine, kGap);
+}
+
+// The first `per_bucket` CTAs write the buckets of the offsets, the others one head's values each.
+template <typename T>
+__global__ void __launch_bounds__(kMost) expand_kernel(const Borders b, const T *__restrict__ table, int H, int buckets,
+                                                       int R, int per_bucket, float *__restrict__ tab,
+                                                       uint8_t *__restrict__ bm) {
+    __shared__ float s[kMost], sorted[kMost], place[kMost], tops[kMost / 32], lows[kMost / 32];
+    const int k = threadIdx.x, h = static_cast<int>(blockIdx.x) - per_bucket;
+    grid_release();
+    if (h < 0) {
+        const int x = blockIdx.x * kMost + k;
+        if (x <= 2 * R) bm[x] = static_cast<uint8_t>(bucket_of(x - R, b));
+        return;
+    }
+    float x = -INFINITY;
+    if (k < buckets) x = static_cast<float>(table[static_cast<size_t>(k) * H + h]);
+    if (x < kMask) x = -INFINITY;
+    s[k] = x;
+    float top = is_finite(x) ? x : -INFINITY, low = is_finite(x) ? x : INFINITY;
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+    }
+    if ((k & 31) == 0) {
+        tops[k >> 5] = top;
+        lows[k >> 5] = low;
+    }
+    __syncthreads();
+    #pragma unroll
+    for (int w = 0; w < kMost / 32; ++w) {
+        top = fmaxf(top, tops[w]);
+        low = fminf(low, lows[w]);
+    }
+    // usual entries stay as they are; a head of masks alone has neither top nor low
+    if (top > -INFINITY && (top - low > kGap || fabsf(top) > kGap)) x = closer(s, buckets, k, top, low, sorted, place);
+    if (k < buckets) tab[static_cast<size_t>(h) * buckets + k] = x * 1.4426950408889634f;
 }
 
 // dtable[b][h]: the partial sums [B, H, per, buckets] over the batch and the
@@ -103,11 +181,11 @@ cudaError_t launch_bias_expand(const void *table, bool f32, int H, int S, int bu
     float *t = static_cast<float *>(workspace);
     uint8_t *m = static_cast<uint8_t *>(workspace) + up256(static_cast<size_t>(H) * buckets * 4);
     const Borders b = make_borders(buckets, far);
-    const int n = 2 * R + 1 > H * buckets ? 2 * R + 1 : H * buckets;
+    const int per_bucket = (2 * R + kMost) / kMost, grid = per_bucket + H;
     if (f32)
-        expand_kernel<<<(n + 255) / 256, 256, 0, st>>>(b, static_cast<const float *>(table), H, buckets, R, t, m);
+        expand_kernel<<<grid, kMost, 0, st>>>(b, static_cast<const float *>(table), H, buckets, R, per_bucket, t, m);
     else
-        expand_kernel<<<(n + 255) / 256, 256, 0, st>>>(b, static_cast<const __nv_bfloat16 *>(table), H, buckets, R, t, m);
+        expand_kernel<<<grid, kMost, 0, st>>>(b, static_cast<const __nv_bfloat16 *>(table), H, buckets, R, per_bucket, t, m);
     *tab = t;
     *bm = m + R;  // offset 0
     return cudaGetLastError();

@@ -529,7 +529,16 @@ vsa_status vsa_block_sparse_attention_tiled_backward(const void *dout, const voi
  * bucket(r) = f(|r|) + (n if r > 0): short distances have a bucket each,
  * longer ones share buckets that widen with the distance, and everything from
  * max_distance on is in the last one.
- *   lse        output as above, or NULL
+ *              Entries of any size are taken: -inf and entries below -2^127
+ *              mask their bucket (so does the lowest value of either type),
+ *              entries above 2^127 are not for use.  A row without any other
+ *              entry sees no key.
+ *   lse        output as above, or NULL.  Where the sorted entries of a head
+ *              lie more than 2839 apart, lse counts that distance
+ *              as 2839, and a head's largest entry as 0 if it is beyond
+ *              +-2839: at such sizes fp32 holds no logarithm of a sum.  No
+ *              probability depends on it while scaled products of one row
+ *              differ by less than 2700.
  *   bias       [num_buckets, n_heads] in bias_dtype, or NULL (num_buckets and
  *              max_distance are then ignored and workspace may be NULL)
  *   num_buckets even, in [4, 256]; max_distance in (num_buckets / 4, 2^24]

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import block_sparse_self_b200 as vsa
-from test_gpu_backward import DEV, U, check, inputs, reference, window_mask
+from test_gpu_backward import DEV, U, bucket_of, check, inputs, reference, window_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,77 @@ def test_center_of_a_vanishing_mass(mode):
     mass = 16 * math.exp(-86)
     assert (ref["e_dX"].sum(1) / mass).max() > torch.finfo(torch.float32).max
     check([x[0, 0] for x in got], ref)
+
+
+# --------------------------------------------------------------------------
+# bias entries of any size
+# --------------------------------------------------------------------------
+
+def buckets_of(S, buckets, far):
+    f = torch.tensor([bucket_of(d, buckets, far) for d in range(far + 1)], device=DEV)
+    i = torch.arange(S, device=DEV)
+    r = i[None, :] - i[:, None]
+    return f[r.abs().clamp(max=far)] + (r > 0) * (buckets // 2)
+
+
+def large_tables(low, table):
+    """Heads whose rows, some or all, see nothing but entries of the size of `low` (negative)."""
+    b = torch.randn(16, 5, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    b[:8, 0] = low                    # masked by sign, the own key too: the last row sees masked keys only
+    b[:, 1] += low                    # every entry: a common shift changes nothing
+    b[0, 2] = -low                    # the own key far above everything else
+    b[:4, 3] = low                    # three levels, the own key on the lowest: rows with three kinds of best key
+    b[4:8, 3] = low / 2
+    b[9:, 4] = 3 * low                # two levels, and single entries below the own key's
+    b[3, 4] = low
+    return b.to(table)
+
+
+@pytest.mark.parametrize("low,table", [(-1e4, torch.float32), (-1e7, torch.float32), (-1e8, torch.bfloat16),
+                                       (-1e9, torch.float32), (-1e30, torch.float32), (-5e37, torch.bfloat16)])
+@pytest.mark.parametrize("S,D,window,sink", [(300, 64, 120, 2), (200, 128, 200, 0), (130, 64, 1, 0)])
+def test_bias_entries_of_any_size(S, D, window, sink, low, table):
+    """The softmax does not depend on the size of entries that a row sees nothing beside.
+
+    Rows below one or two gaps have logits of up to 2^13 in the kernels (log2 units): rounding half a unit in the last
+    place, 2^-11, four times (the saved logarithm twice, on its way to log2 units, the logit) moves a probability by
+    4 ln 2 2^-11 < 0.36 u on top of the (2 + 1/16) u of the bounds: times 1.2."""
+    H, far = 5, 64
+    q, k, v, g = inputs(1, H, S, D, seed=S + 7)
+    bias = large_tables(low, table)
+    o, lse, o_lo = vsa.window_attention(q, k, v, window, sink, bias=bias, max_distance=far, return_remainder=True)
+    *grads, dbias = vsa.window_attention_backward(g, q, k, v, o, lse, window, sink, bias=bias, max_distance=far,
+                                                  grad_dtype=torch.float32, o_lo=o_lo)
+    assert lse.isfinite().all()
+    bucket, see = buckets_of(S, 16, far), window_mask(S, window, sink)
+    want, err = (torch.zeros(16, H, dtype=torch.float64, device=DEV) for _ in range(2))
+    for h in range(H):
+        b = bias[:, h].double()[bucket]
+        b -= b.masked_fill(~see, -math.inf).amax(1, keepdim=True)   # 64 bits do not hold a logit beside 1e30 either
+        ref = reference(q[0, h], k[0, h], v[0, h], g[0, h], see, None, b)
+        for name in ("o", "dq", "dk", "dv", "dX"):
+            ref["e_" + name] = 1.2 * ref["e_" + name]
+        assert ((o[0, h].double() - ref["o"]).abs() <= ref["e_o"] + 1e-6).all(), h
+        check([x[0, h] for x in grads], ref, what=f"head {h}")
+        want[:, h].index_add_(0, bucket.view(-1), ref["dX"].view(-1))
+        err[:, h].index_add_(0, bucket.view(-1), ref["e_dX"].view(-1))
+    if table == torch.bfloat16:
+        err += U * (want.abs() + err)
+    assert ((dbias.double() - want).abs() <= err + 1e-6).all()
+
+
+def test_large_entries_leave_the_others_alone():
+    """A mask by a large entry gives the bits of a mask by -inf where every row has another key, lse included."""
+    S, D, H, far = 300, 64, 2, 64
+    q, k, v, g = inputs(1, H, S, D, seed=31)
+    bias = torch.randn(16, H, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    res = []
+    for low in (-math.inf, -1e9, -1e4, torch.finfo(torch.float32).min):
+        b = bias.clone()
+        b[8:, 0] = low
+        b[3, 1] = low
+        o, lse = vsa.window_attention(q, k, v, 120, 2, bias=b, max_distance=far, return_lse=True)
+        res.append((o, lse, *vsa.window_attention_backward(g, q, k, v, o, lse, 120, 2, bias=b, max_distance=far)))
+    for other in res[1:]:
+        for x, y in zip(res[0], other):
+            assert torch.equal(x, y)
