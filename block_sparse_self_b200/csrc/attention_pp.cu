@@ -550,7 +550,12 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 const int b0 = __shfl_sync(0xffffffffu, bk[4], 0);
                 flat = __all_sync(0xffffffffu, bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
                 if (flat) add = sTab[b0];
-                else mul = 1.f;
+                // NaN and +inf go in ahead of the mask, which takes them out again
+                flat = flat && add < INFINITY;
+                if (!flat) {
+                    add = 0.f;
+                    mul = 1.f;
+                }
             }
             auto apply_bias = [&]() {
                 if constexpr (BIAS) {

@@ -353,6 +353,14 @@ bwd_dkv_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, co
                         for (int u = 0; u < 2; ++u)
                             see[u] = span_bits(q0 + 64 * hf + 32 * u, p - a.half, p + a.half + 1);
                     }
+                    if constexpr (BIAS) {
+                        // rows past the last have lse = +inf, which a NaN entry of the bias would turn into NaN
+                        if (q0 + 128 > a.P) {
+                            masked = true;
+                            #pragma unroll
+                            for (int u = 0; u < 2; ++u) see[u] &= span_bits(q0 + 64 * hf + 32 * u, 0, a.P);
+                        }
+                    }
                 } else if (a.group > 0 || a.gstride > 1) {
                     masked = true;
                     #pragma unroll

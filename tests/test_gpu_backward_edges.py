@@ -125,3 +125,47 @@ def test_large_entries_leave_the_others_alone():
     for other in res[1:]:
         for x, y in zip(res[0], other):
             assert torch.equal(x, y)
+
+
+# --------------------------------------------------------------------------
+# entries that are not finite
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("S,window,sink", [(16, 16, 0), (200, 40, 0), (300, 40, 3), (517, 100, 0)])
+def test_bias_entries_that_are_not_finite_stay_with_their_pairs(S, window, sink, bad):
+    """A NaN (or +inf) entry reaches the rows that see its bucket, the keys that those rows see, and nothing else.
+    (At S = 16 offset 16, the first of a bucket, is that of positions past the end alone.)"""
+    D, far = 64, 64
+    q, k, v, g = inputs(1, 1, S, D, seed=32)
+    table = torch.randn(16, 1, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    table[2] = -1e9             # with a gap to close
+    bucket, see = buckets_of(S, 16, far), window_mask(S, window, sink)
+    tile = torch.arange(S, device=DEV) // 128
+    meet = torch.zeros(int(tile[-1]) + 1, int(tile[-1]) + 1, dtype=torch.bool, device=DEV)
+    i, j = see.nonzero(as_tuple=True)
+    meet[tile[i], tile[j]] = True       # tiles of queries and keys that are computed together
+
+    def step(b):
+        o, lse = vsa.window_attention(q, k, v, window, sink, bias=b, max_distance=far, return_lse=True)
+        grads = vsa.window_attention_backward(g, q, k, v, o, lse, window, sink, bias=b, max_distance=far)
+        return [x[0, 0] for x in (o, *grads[:3])] + [grads[3]]
+
+    clean = step(table)
+    for at in (15, 14, 9, 7, 6):
+        b = table.clone()
+        b[at] = bad
+        o, dq, dk, dv, db = step(b)
+        hit = ((bucket == at) & see).any(1)
+        seen = (hit[:, None] & see).any(0)
+        assert o[hit].isnan().all() and dq[hit].isnan().all() and dk[seen].isnan().all() and dv[seen].isnan().all()
+        assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(dv[~seen], clean[3][~seen])
+        # the center of dq's rows changes with the masses of the rows that are gone: rounding only
+        assert ((dq - clean[1])[~hit].abs() <= 2 * U * clean[1].abs().max()).all()
+        # a masked pair of a computed tile is zero times the lost row's delta
+        near = torch.stack([hit[tile == t].any() for t in range(len(meet))])
+        far_keys = ~(near[:, None] & meet).any(0)[tile]
+        assert torch.equal(dk[far_keys], clean[2][far_keys])
+        if not hit.any():
+            others = torch.arange(16, device=DEV) != at
+            assert torch.equal(dq, clean[1]) and torch.equal(db[others], clean[4][others]) and not db[at].any()
