@@ -263,6 +263,13 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // a head with an entry of NaN or +inf adds every bias ahead of the mask, which takes
+    // it out again where the pair is masked (tested per tile it cost 2.6 % at S = 30720)
+    [[maybe_unused]] bool usual = true;
+    if constexpr (BIAS) {
+        for (int b = lane; b < a.buckets; b += 32) usual = usual && sTab[b] < INFINITY;
+        usual = __all_sync(0xffffffffu, usual);
+    }
     const uint32_t tmem = *tmem_slot;
     bool bad[2] = {false, false};
     for (int t = 0; t < 2; ++t) {
@@ -548,14 +555,9 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             [[maybe_unused]] bool flat = true;
             if constexpr (BIAS) {
                 const int b0 = __shfl_sync(0xffffffffu, bk[4], 0);
-                flat = __all_sync(0xffffffffu, bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
+                flat = usual && __all_sync(0xffffffffu, bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
                 if (flat) add = sTab[b0];
-                // NaN and +inf go in ahead of the mask, which takes them out again
-                flat = flat && add < INFINITY;
-                if (!flat) {
-                    add = 0.f;
-                    mul = 1.f;
-                }
+                else mul = 1.f;
             }
             auto apply_bias = [&]() {
                 if constexpr (BIAS) {
