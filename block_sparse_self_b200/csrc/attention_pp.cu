@@ -184,7 +184,12 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // grid, 4 heads, 64-token tiles, 62 blocks listed), the same 89 us at D = 64 (2 x 5
 // heads of 120 blocks, 14 listed).  The columns past a list's end repeat its last
 // block, masked.
-template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false, int BS = 128>
+//
+// LSE: the row's log-sum-exp is written.  It is a statistic of its own (the backward
+// pass recomputes P from it), so it is taken from a second sum of the unrounded
+// exponentials: O's sum adds them as PV does, rounded to bf16, which puts a row that
+// a few keys of a later block hold off by up to 2^-9.
+template <int D, bool WINDOW, bool TILED, bool PAD, bool BIAS = false, int BS = 128, bool LSE = BS != 128>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     using C = PPCfg<D>;
@@ -470,6 +475,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
         const uint32_t s_col = t * 128, o_col = C::O_COL + t * D;
         const float sl2 = a.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
+        [[maybe_unused]] float l_exact = 0.f;  // LSE: the sum before rounding
         // buckets of a key tile's five runs of 32 offsets (this lane's of each)
         [[maybe_unused]] int bk[5] = {0, 0, 0, 0, 0};
         [[maybe_unused]] auto fetch_buckets = [&](int j) {
@@ -650,19 +656,32 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             // rounding error in its weights' total.  The mixed-precision adds take
             // each half of the packed pair as it is; unpacking the pair first for
             // two-wide adds measured a few percent slower.
+            [[maybe_unused]] float rs_exact = 0.f;
             auto exp_pass = [&](float m_use) -> float {
                 const float f = BIAS ? mul : sl2, c0 = BIAS ? add - m_use : -m_use;
                 const uint64_t sl2x2 = f32x2(f, f), nmx2 = f32x2(c0, c0);
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                [[maybe_unused]] uint64_t e0 = 0, e1 = 0;  // two pairs of fp32 zeros
                 #pragma unroll
                 for (int q = 0; q < BN / 2; ++q) {
                     float a0, a1;
                     f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), sl2x2, nmx2),
                                 a0, a1);
-                    const uint32_t pk = pack_bf16x2(ex2_approx(a0), ex2_approx(a1));
+                    a0 = ex2_approx(a0);
+                    a1 = ex2_approx(a1);
+                    const uint32_t pk = pack_bf16x2(a0, a1);
                     if (q & 1) add_bf16x2_f32(pk, s2, s3);
                     else add_bf16x2_f32(pk, s0, s1);
+                    if constexpr (LSE) {
+                        if (q & 1) e1 = add_f32x2(e1, f32x2(a0, a1));
+                        else e0 = add_f32x2(e0, f32x2(a0, a1));
+                    }
                     x[q] = pk;   // P, packed in place (q <= 2q)
+                }
+                if constexpr (LSE) {
+                    float t0, t1;
+                    f32x2_split(add_f32x2(e0, e1), t0, t1);
+                    rs_exact = t0 + t1;
                 }
                 return (s0 + s2) + (s1 + s3);
             };
@@ -711,6 +730,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                         }
                         tmem_st_wait();
                         l_sum *= alpha;
+                        if constexpr (LSE) l_exact *= alpha;
                     }
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -721,6 +741,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
                 if (j + 1 < n) fetch_buckets(j + 1);
             }
             l_sum += rs;
+            if constexpr (LSE) l_exact += rs_exact;
             // P over the first 64 columns of this tile's S
             tmem_st32(t_lane + s_col, *reinterpret_cast<const uint32_t(*)[32]>(&x[0]));
             tmem_st32(t_lane + s_col + 32, *reinterpret_cast<const uint32_t(*)[32]>(&x[32]));
@@ -769,10 +790,12 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);
             if (a.stats && row_valid) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(m_ref, l_sum);
-            if (a.lse && row_valid) a.lse[orow] = row_lse(m_ref, l_sum);
+            if constexpr (LSE) {
+                if (row_valid) a.lse[orow] = row_lse(m_ref, l_exact);
+            }
         } else if (row_valid && bad[t]) {
             if (a.stats) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(-INFINITY, 0.f);
-            if (a.lse) a.lse[orow] = -INFINITY;
+            if constexpr (LSE) a.lse[orow] = -INFINITY;
             if (a.out_f32) {
                 float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
                 for (int e = 0; e < D / 4; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -795,8 +818,8 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     }
 }
 
-template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false, int BS = 128>
-vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
+template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false, int BS = 128, bool LSE = BS != 128>
+vsa_status run_kept(const AttnLaunch &L, int *status, cudaStream_t st) {
     using C = PPCfg<D>;
     MapSet maps = {};  // copied into the launch parameters
     bool ok = true;
@@ -814,7 +837,7 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
              make_tile_map(&maps.v[0], L.v, D, L.S, L.BH, BS);
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
-    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS, BS>;
+    auto kern = attn_pp_kernel<D, WINDOW, TILED, PAD, BIAS, BS, LSE>;
     constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -883,6 +906,12 @@ vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
     return check_cuda(cudaGetLastError(), "attention launch (two tiles)");
 }
 
+template <int D, bool WINDOW, bool TILED, bool PAD = false, bool BIAS = false>
+vsa_status run_pp(const AttnLaunch &L, int *status, cudaStream_t st) {
+    return L.lse ? run_kept<D, WINDOW, TILED, PAD, BIAS, 128, true>(L, status, st)
+                 : run_kept<D, WINDOW, TILED, PAD, BIAS, 128, false>(L, status, st);
+}
+
 // Lists of one key block (such as the temporal-only mask's diagonal): the
 // work is HBM bound (Q, K and V read and O written once per query tile), so
 // what matters is keeping loads in flight.  Persistent CTAs, two per SM, take
@@ -910,7 +939,8 @@ constexpr int kOneThreads = 192;  // warps 0-3 softmax/epilogue, 4 TMA producer,
 
 // At most 160 registers a thread, so that two CTAs (12 warps) fit in the
 // SM's register file beside each other.
-template <int D, bool WINDOW, bool TILED, bool PAD>
+// LSE as for the two-tile kernel.
+template <int D, bool WINDOW, bool TILED, bool PAD, bool LSE>
 __global__ void __maxnreg__(160)
 attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     static_assert(!WINDOW, "window attention always takes the two-tile kernel");
@@ -1126,7 +1156,7 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             if (sc.n == 0) {
                 if (row_valid && T.bad) {
                     if (a.stats) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(-INFINITY, 0.f);
-                    if (a.lse) a.lse[orow] = -INFINITY;
+                    if constexpr (LSE) a.lse[orow] = -INFINITY;
                     if (a.out_f32) {
                         float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + orow * D);
                         for (int e = 0; e < D / 4; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1197,14 +1227,21 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
             const uint64_t sl2x2 = f32x2(sl2, sl2), nmx2 = f32x2(-m_use, -m_use);
             float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            [[maybe_unused]] uint64_t e0 = 0, e1 = 0;  // two pairs of fp32 zeros
             #pragma unroll
             for (int q = 0; q < BN / 2; ++q) {
                 float a0, a1;
                 f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1])), sl2x2, nmx2),
                             a0, a1);
-                const uint32_t pk = pack_bf16x2(ex2_approx(a0), ex2_approx(a1));
+                a0 = ex2_approx(a0);
+                a1 = ex2_approx(a1);
+                const uint32_t pk = pack_bf16x2(a0, a1);
                 if (q & 1) add_bf16x2_f32(pk, s2, s3);
                 else add_bf16x2_f32(pk, s0, s1);
+                if constexpr (LSE) {
+                    if (q & 1) e1 = add_f32x2(e1, f32x2(a0, a1));
+                    else e0 = add_f32x2(e0, f32x2(a0, a1));
+                }
                 x[q] = pk;   // P, packed in place (q <= 2q)
             }
             // P over the first 64 columns of S
@@ -1253,7 +1290,11 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             }
             if (row_valid && l_sum <= 0.f) report(a.status, DEV_RUNTIME);
             if (a.stats && row_valid) a.stats[static_cast<size_t>(bh) * a.S + rg] = make_float2(m_ref, l_sum);
-            if (a.lse && row_valid) a.lse[orow] = row_lse(m_ref, l_sum);
+            if constexpr (LSE) {
+                float t0, t1;
+                f32x2_split(add_f32x2(e0, e1), t0, t1);
+                if (row_valid) a.lse[orow] = row_lse(m_ref, t0 + t1);
+            }
             ++w;
         }
         if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
@@ -1267,8 +1308,8 @@ attn_one_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
     }
 }
 
-template <int D, bool TILED, bool PAD = false>
-vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
+template <int D, bool TILED, bool PAD, bool LSE>
+vsa_status run_one_kept(const AttnLaunch &L, int *status, cudaStream_t st) {
     constexpr bool WINDOW = false;
     using C = OneCfg<D>;
     // with one S buffer, QK(1) would wait for PV(0), which is issued after it:
@@ -1290,7 +1331,7 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
              make_tile_map(&maps.v[0], L.v, D, L.S, L.BH, 128);
     }
     if (!ok) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point or arguments)");
-    auto kern = attn_one_kernel<D, WINDOW, TILED, PAD>;
+    auto kern = attn_one_kernel<D, WINDOW, TILED, PAD, LSE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention, one key block)");
     PPArgs a;
@@ -1369,11 +1410,16 @@ vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
     return check_cuda(cudaGetLastError(), "attention launch (one key block)");
 }
 
+template <int D, bool TILED, bool PAD = false>
+vsa_status run_one(const AttnLaunch &L, int *status, cudaStream_t st) {
+    return L.lse ? run_one_kept<D, TILED, PAD, true>(L, status, st) : run_one_kept<D, TILED, PAD, false>(L, status, st);
+}
+
 template <int D, int BS>
 vsa_status run_short(const AttnLaunch &L, bool pad, int *status, cudaStream_t st) {
-    if (!L.tiled) return run_pp<D, false, false, false, false, BS>(L, status, st);
-    return pad ? run_pp<D, false, true, true, false, BS>(L, status, st)
-               : run_pp<D, false, true, false, false, BS>(L, status, st);
+    if (!L.tiled) return run_kept<D, false, false, false, false, BS>(L, status, st);
+    return pad ? run_kept<D, false, true, true, false, BS>(L, status, st)
+               : run_kept<D, false, true, false, false, BS>(L, status, st);
 }
 
 }  // namespace

@@ -469,7 +469,7 @@ vsa_status vsa_head_profile(const void *q, const void *k, int B, int n_heads, in
  * The forward calls with _lse in their names are the calls above with one
  * more output, lse [B, n_heads, S] fp32: per row of o the natural logarithm
  * of the sum behind its softmax (-inf for a row that saw no key, whose o is
- * zero).  o is the same bit for bit, except for blocks of 32 and 64 tokens,
+ * zero), from fp32 exponentials as they are before P is rounded.  o is the same bit for bit, except for blocks of 32 and 64 tokens,
  * which run on another kernel here and round differently.  o_lo (NULL, or [B, n_heads, S, D] bf16
  * beside a bf16 o) receives what rounding o to bf16 left; given to the
  * backward call it makes delta below as exact as an fp32 o would, which dq

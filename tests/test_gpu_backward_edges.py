@@ -170,3 +170,44 @@ def test_bias_entries_that_are_not_finite_stay_with_their_pairs(S, window, sink,
         assert close(dk, "dk", ~(near[:, None] & meet).any(0)[tile])
         if not hit.any():
             assert ((db[:, 0].double() - want_db).abs() <= err_db + 1e-5).all() and not db[at].any()
+
+
+# --------------------------------------------------------------------------
+# lse
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("mode,block,nb,D", [("lists", 128, 6, 128), ("lists", 64, 9, 64), ("lists", 32, 14, 128),
+                                             ("lists", 128, 1, 64), ("tiled", 128, 8, 64), ("tiled", 64, 12, 128),
+                                             ("window", 128, 5, 128), ("bias", 128, 5, 64)])
+def test_lse_is_that_of_unrounded_exponentials(mode, block, nb, D):
+    """Rows that a few keys of a later block hold: the bf16 rounding of their exponentials must not reach lse.
+
+    With logits up to x = scale sum |q_d k_d| the accumulation of a product is off by D 2^-24 x at most, a sum of
+    S <= 1024 exponentials by 2^-14 of itself, 2^x by 2^-22 and the last roundings by 2^-24 (|lse| + |m|), all of it
+    below 2^-11 here (x <= 40).  P then carries its own rounding alone: |err dv_j| <= (u + u/16) sum_i P_ij |g_i|."""
+    H, S = 2, block * nb
+    q, k, v, g = inputs(1, H, S, D, seed=50 + S + D)
+    q = (2 * q.float()).bfloat16()
+    see, bias, args, kw = torch.ones(S, S, dtype=torch.bool, device=DEV), None, (), {}
+    if mode in ("window", "bias"):
+        fwd, bwd, args = vsa.window_attention, vsa.window_attention_backward, (200, 9)
+        see = window_mask(S, 200, 9)
+        if mode == "bias":
+            table = torch.randn(16, H, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+            kw, bias = dict(bias=table, max_distance=64), table.double()[buckets_of(S, 16, 64)]
+    else:
+        idx = torch.arange(nb, dtype=torch.int32, device=DEV).expand(nb, nb).contiguous()
+        cnt = torch.full((nb,), nb, dtype=torch.int32, device=DEV)
+        fwd, bwd, args = vsa.block_sparse_attention, vsa.block_sparse_attention_backward, (idx, cnt, block)
+        if mode == "tiled":
+            grid = (nb, 8, block // 8)
+            fwd, bwd = vsa.block_sparse_attention_tiled, vsa.block_sparse_attention_tiled_backward
+            args = (grid, [(1, 8, block // 8)], None, idx, cnt)
+    o, lse = fwd(q, k, v, *args, out_dtype=torch.float32, return_lse=True, **kw)
+    dv = bwd(g, q, k, v, o, lse, *args, grad_dtype=torch.float32, **kw)[2]
+    for h in range(H):
+        assert (q[0, h].abs().float() @ k[0, h].abs().float().T).max() / math.sqrt(D) <= 40
+        ref = reference(q[0, h], k[0, h], v[0, h], g[0, h], see, None, None if bias is None else bias[:, :, h])
+        assert (lse[0, h].double() - ref["lse"]).abs().max() <= 2.0 ** -11
+        ref["e_dv"] = ref["e_dv"] * (1 + 1 / 16) / (2 + 1 / 16)
+        check([dv[0, h]], ref, names=("dv",))
