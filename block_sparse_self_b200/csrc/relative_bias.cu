@@ -6,7 +6,7 @@
 //   f(d) = d for d < e, else min(n - 1, e + floor((n - e) ln(d / e) / ln(far / e))),
 // bucket(r) = f(|r|) + (n if r > 0).  f steps up where d reaches
 // e (far / e)^(t / (n - e)); those borders are rounded up to whole numbers on
-// the host, so the kernels only compare integers.
+// the host (exactly), so the kernels only compare integers.
 //
 // The attention kernels read bucket(r) as a byte, for |r| <= R = min(far, S)
 // (larger offsets fall into the last bucket of their side), and each head's
@@ -24,6 +24,8 @@
 // to anything between 0.2 and 5200.
 // Every row sees its own key, so nothing below that key's bucket needs an order of
 // its own: all that is more than the gap below it is put at the gap.
+#include <math.h>
+
 #include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -37,16 +39,49 @@ struct Borders {
     int at[128];
 };
 
+// A whole number of up to 2048 bits.
+struct Whole {
+    uint32_t w[64] = {1};
+    int n = 1;  // words in use
+    Whole &times(uint32_t x, int power) {
+        for (; power > 0; --power) {
+            uint64_t carry = 0;
+            for (int i = 0; i < n; ++i) {
+                carry += static_cast<uint64_t>(w[i]) * x;
+                w[i] = static_cast<uint32_t>(carry);
+                carry >>= 32;
+            }
+            if (carry) w[n++] = static_cast<uint32_t>(carry);
+        }
+        return *this;
+    }
+    bool operator>=(const Whole &o) const {
+        if (n != o.n) return n > o.n;
+        for (int i = n - 1; i > 0; --i)
+            if (w[i] != o.w[i]) return w[i] > o.w[i];
+        return w[0] >= o.w[0];
+    }
+};
+
+// Whether d >= e (far / e)^(t / m), by whole numbers: d^m >= e^(m-t) far^t (at most
+// 25 x 64 bits).
+bool reaches(int d, int e, int far, int t, int m) {
+    return Whole().times(d, m) >= Whole().times(e, m - t).times(far, t);
+}
+
 Borders make_borders(int buckets, int far) {
     Borders b{};
     b.n = buckets / 2;
     b.e = b.n / 2;
     const int m = b.n - b.e;
     for (int t = 1; t < m; ++t) {
-        // a border that is a whole number must not be rounded up to the next
         const long double x = static_cast<long double>(b.e) *
                               powl(static_cast<long double>(far) / b.e, static_cast<long double>(t) / m);
-        b.at[b.steps++] = static_cast<int>(ceill(x * (1.0L - 1e-13L)));
+        // a border next to a whole number is that number or a little above it, which
+        // no rounded power tells
+        const int near = static_cast<int>(rintl(x));
+        b.at[b.steps++] = fabsl(x - near) > 1e-12L * x ? static_cast<int>(ceill(x))
+                                                       : reaches(near, b.e, far, t, m) ? near : near + 1;
     }
     return b;
 }

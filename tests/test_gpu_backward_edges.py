@@ -211,3 +211,18 @@ def test_lse_is_that_of_unrounded_exponentials(mode, block, nb, D):
         assert (lse[0, h].double() - ref["lse"]).abs().max() <= 2.0 ** -11
         ref["e_dv"] = ref["e_dv"] * (1 + 1 / 16) / (2 + 1 / 16)
         check([dv[0, h]], ref, names=("dv",))
+
+
+# --------------------------------------------------------------------------
+# buckets
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("buckets,far,border", [(96, 4010233, 198349), (106, 8670623, 125033), (244, 13223778, 352201),
+                                                (36, 6102237, 1372691), (32, 128, 64), (64, 4096, 512), (20, 2560, 320)])
+def test_bucket_borders_next_to_whole_numbers(buckets, far, border):
+    """Borders that lie within 10^-13 above a whole number (it is still in the lower bucket), and on one."""
+    got = vsa.relative_position_buckets(buckets, far)
+    for d in (border - 1, border, border + 1, border + 2):
+        if d <= far:
+            assert int(got[far - d]) == bucket_of(d, buckets, far)
+            assert int(got[far + d]) == buckets // 2 + bucket_of(d, buckets, far)
