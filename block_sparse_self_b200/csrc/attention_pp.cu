@@ -842,7 +842,7 @@ vsa_status run_kept(const AttnLaunch &L, int *status, cudaStream_t st) {
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention, two tiles)");
-    PPArgs a;
+    PPArgs a{};
     const int positions = TILED ? L.Tp * L.Hp * L.Wp : L.S;
     a.S = positions;
     a.S_out = L.S;
@@ -1334,7 +1334,7 @@ vsa_status run_one_kept(const AttnLaunch &L, int *status, cudaStream_t st) {
     auto kern = attn_one_kernel<D, WINDOW, TILED, PAD, LSE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return check_cuda(e, "cudaFuncSetAttribute(attention, one key block)");
-    PPArgs a;
+    PPArgs a{};
     const int positions = TILED ? L.Tp * L.Hp * L.Wp : L.S;
     a.S = positions;
     a.S_out = L.S;
@@ -1348,20 +1348,12 @@ vsa_status run_one_kept(const AttnLaunch &L, int *status, cudaStream_t st) {
     a.group = L.group;
     a.gstride = L.gstride;
     a.nb = L.nb;
-    a.half = L.half;
-    a.sink = L.sink;
-    a.dense = L.dense;
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.out = L.o;
     a.out_f32 = L.out_f32;
     a.stats = L.stats;
     a.lse = L.lse;
     a.o_lo = L.o_lo;
-    a.bias_tab = L.bias_tab;
-    a.buckets = L.buckets;
-    a.bias_bm = L.bias_bm;
-    a.bias_R = L.bias_R;
-    a.n_heads = L.n_heads;
     a.status = status;
     a.H = TILED ? L.Hp : L.Hg;
     a.W = TILED ? L.Wp : L.Wg;
