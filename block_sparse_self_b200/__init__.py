@@ -260,8 +260,9 @@ def _permute(x, grid, tiles, choice, inverse):
                          f"({'padded' if inverse else 'real'} tokens of grid {tuple(grid)})")
     y = torch.empty(B, H, S if inverse else Sp, D, dtype=x.dtype, device=x.device)
     fn = lib().vsa_unpermute if inverse else lib().vsa_permute
-    _check(fn(_ptr(x), _ptr(y), _dtype_code(x, "x"), B, H, S, D, Dims3(*grid), arr, n, _ptr(choice),
-              _stream(x.device)))
+    with _on(x):
+        _check(fn(_ptr(x), _ptr(y), _dtype_code(x, "x"), B, H, S, D, Dims3(*grid), arr, n, _ptr(choice),
+                  _stream(x.device)))
     return y
 
 
@@ -469,7 +470,8 @@ def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be bfloat16 or float32")
     y = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-    _check(lib().vsa_cast_f32_to_bf16(_ptr(t), _ptr(y), t.numel(), _stream(t.device)))
+    with _on(t):
+        _check(lib().vsa_cast_f32_to_bf16(_ptr(t), _ptr(y), t.numel(), _stream(t.device)))
     return y
 
 

@@ -182,3 +182,54 @@ def test_going_back_through_lse_or_the_remainder_is_an_error(host, monkeypatch, 
         out = vsa.window_attention(leaf, k, v, 64, **kw)
     with pytest.raises(NotImplementedError, match="lse"):
         (out[0].float().sum() + out[what].float().sum() + leaf.float().sum()).backward()
+
+
+class Devices:
+    """_on() that remembers whose device is current."""
+
+    def __init__(self):
+        self.current = []
+
+    def __call__(self, t):
+        self.tensor = t
+        return self
+
+    def __enter__(self):
+        self.current.append(self.tensor)
+
+    def __exit__(self, *a):
+        self.current.pop()
+
+
+@pytest.mark.parametrize("call", ["lists", "tiled", "window", "permute", "unpermute"])
+def test_training_calls_launch_with_their_tensors_device_current(host, monkeypatch, call):
+    """A stream belongs to a device: with another one current a launch on it fails.  Every launch of a recorded call
+    over fp32 inputs, the casts to bf16 among them, is made with the tensors' device current."""
+    on, launched = Devices(), []
+
+    class Runs(Recorder):
+        def __getattr__(self, name):
+            if name == "vsa_padded_grid" or name.endswith("workspace_size"):
+                return getattr(self.real, name)
+
+            def launch(*args):
+                assert on.current, name
+                launched.append(name)
+                return vsa.OK
+            return launch
+
+    real = vsa.lib().real
+    monkeypatch.setattr(vsa, "lib", lambda: Runs(real))
+    monkeypatch.setattr(vsa, "_on", on)
+    q, k, v = (x.float().requires_grad_() for x in qkv(B, H, math.prod(GRID)))
+    if call == "lists":
+        o = vsa.block_sparse_attention(q, k, v, *lists(B, H, NB), 128)
+    elif call == "tiled":
+        o = vsa.block_sparse_attention_tiled(q, k, v, GRID, TILES, None, *lists(B, H, NB))
+    elif call == "window":
+        o = vsa.window_attention(q, k, v, 64, bias=torch.zeros(8, H, requires_grad=True), max_distance=16)
+    else:
+        o = getattr(vsa, call)(q, GRID, TILES)
+    forward = len(launched)
+    o.sum().backward()
+    assert forward >= 1 and len(launched) > forward
