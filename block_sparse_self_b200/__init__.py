@@ -681,7 +681,8 @@ def block_sparse_attention_backward(do, q, k, v, o, lse, idx, cnt, block: int, g
                                     o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention for the gradient `do` of its output, from that output
     and its lse (and its remainder o_lo, if the forward call returned one).  The gradients have q's
-    type unless grad_dtype says otherwise."""
+    type unless grad_dtype says otherwise.  o and lse may also be joined from several calls over parts
+    of the keys: each part's call then gives its share of dq, and dk and dv of its keys."""
     _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
     _check_saved(do, q, o, lse, o_lo)

@@ -1,7 +1,7 @@
 // backward.cu -- the steps around the backward pass's two tensor-core passes:
 // per-row statistics, workspace, tensor maps and launches.
 //
-// Row statistics: delta_i = g_i.o_i, one pass over g and o (bandwidth bound:
+// Row statistics: delta_i = g_i.o_i and the size of its error, one pass over g and o (bandwidth bound:
 // 2 x 2 S D bytes per head in bf16), written in position order beside -lse so
 // that both passes read 128 consecutive values per tile whatever the tiling.
 // Positions that hold no token and rows whose forward pass saw no key get
@@ -20,7 +20,7 @@ struct StatArgs {
     RealGrid real;
     int tiled, n_tiles;
     const int32_t *choice;
-    float *nlse, *ndelta, *none;
+    float *nlse, *ndelta, *slack, *none;
     uint32_t *valid;  // nullptr when every position holds a token
 };
 
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     const uint32_t bits = __ballot_sync(0xffffffffu, tok >= 0);
     if (a.valid && lane == 0) a.valid[static_cast<size_t>(bh) * (a.Pw / 32) + p0 / 32] = bits;
     const int sub = lane / LPR, at = lane % LPR;
-    float delta = 0.f;
+    float delta = 0.f, size = 0.f;  // sums of g o and |g o|
     // eight groups of rows at a time: all their loads first (rows without a
     // token load the head's first row and count as zero)
     constexpr int U = 8;
@@ -92,19 +92,28 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
                     o[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u) + __uint_as_float(y[c] & 0xffff0000u);
                 }
             }
-            float s = 0.f;
+            float s = 0.f, n = 0.f;
             #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                s = fmaf(__uint_as_float(gw[c] << 16), o[2 * c], s);
-                s = fmaf(__uint_as_float(gw[c] & 0xffff0000u), o[2 * c + 1], s);
+                const float g0 = __uint_as_float(gw[c] << 16), g1 = __uint_as_float(gw[c] & 0xffff0000u);
+                s = fmaf(g0, o[2 * c], s);
+                s = fmaf(g1, o[2 * c + 1], s);
+                n = fmaf(fabsf(g0), fabsf(o[2 * c]), n);
+                n = fmaf(fabsf(g1), fabsf(o[2 * c + 1]), n);
             }
             #pragma unroll
-            for (int m = LPR / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            for (int m = LPR / 2; m > 0; m >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, m);
+                n += __shfl_xor_sync(0xffffffffu, n, m);
+            }
             // lane r0 + u ROWS + v keeps that row's sum, held by the lanes of group v
             #pragma unroll
             for (int v = 0; v < ROWS; ++v) {
-                const float t = __shfl_sync(0xffffffffu, s, v * LPR);
-                if (lane == r0 + u * ROWS + v) delta = t;
+                const float t = __shfl_sync(0xffffffffu, s, v * LPR), z = __shfl_sync(0xffffffffu, n, v * LPR);
+                if (lane == r0 + u * ROWS + v) {
+                    delta = t;
+                    size = z;
+                }
             }
         }
     }
@@ -119,6 +128,7 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const __grid_constant__ 
     const size_t out = static_cast<size_t>(bh) * a.Pw + p;
     a.nlse[out] = nl;
     a.ndelta[out] = -delta;
+    a.slack[out] = kSlack * size;
     grid_wait();
 }
 
@@ -175,7 +185,7 @@ __global__ void __launch_bounds__(256) block_means_kernel(const __grid_constant_
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t nlse, ndelta, none, valid, kmean, t_off, t_rows, bits, part, bias, total;
+    size_t nlse, ndelta, slack, none, valid, kmean, t_off, t_rows, bits, part, bias, total;
 };
 
 // Whether dQ's rows are centered (backward_dq.cu says what it costs and brings):
@@ -194,6 +204,7 @@ Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, i
     };
     L.nlse = take(BH * Pw * 4);
     L.ndelta = take(BH * Pw * 4);
+    L.slack = take(BH * Pw * 4);
     L.none = take(256 * 4);
     L.valid = take(BH * (Pw / 32) * 4);
     if (centered(lists, cap)) L.kmean = take(BH * (lists > 0 ? nb : Pw / 128) * 128 * 4);  // D <= 128
@@ -247,6 +258,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     a.nlse = f32_at(lay.nlse);
     a.ndelta = f32_at(lay.ndelta);
     a.ndelta_out = f32_at(lay.ndelta);
+    a.slack = f32_at(lay.slack);
     a.none = f32_at(lay.none);
     a.out_f32 = B.grad_f32;
     a.status = status;
@@ -272,6 +284,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     s.choice = L.choice;
     s.nlse = f32_at(lay.nlse);
     s.ndelta = f32_at(lay.ndelta);
+    s.slack = f32_at(lay.slack);
     s.none = f32_at(lay.none);
     s.valid = padded ? reinterpret_cast<uint32_t *>(ws + lay.valid) : nullptr;
 

@@ -9,8 +9,8 @@
 //   dQ_i = scale sum_j dX_ij k_j,  dK_j = scale sum_i dX_ij q_i
 //   dbias[b] = sum over the pairs (i, j) whose offset j - i is in bucket b of dX_ij
 // P is recomputed, never stored.  One pass owns a query block and walks the
-// key blocks of its list (dQ, dbias); the other owns a key block and walks the
-// query blocks that list it (dK, dV).  Each sum has one owner and one order,
+// key blocks of its list (dQ); the other owns a key block and walks the
+// query blocks that list it (dK, dV, dbias).  Each sum has one owner and one order,
 // so results repeat bit for bit and nothing is accumulated in memory; the
 // price is that S and dP are computed in both passes (7 products instead of
 // 5 per pair of blocks).
@@ -21,6 +21,11 @@
 // adds the sum to delta_i, and the dK/dV pass, which runs after it, works with
 // the corrected delta.  dbias is summed there for that reason: it adds up many
 // dX of one sign of error.
+//
+// The sum is that of delta's error only where o and lse belong to the keys that the
+// row walks.  With those of a softmax over more keys (partial results joined) it is a
+// part of the gradient.  delta's error is mostly that of o, half a step of bf16 for its
+// terms, so a sum beyond kSlack sum_d |g_d o_d| is no error: such a row keeps its delta.
 #pragma once
 
 #include <math.h>
@@ -31,6 +36,8 @@
 #include "relative_bias.cuh"
 
 namespace vsa {
+
+constexpr float kSlack = 0x1p-7f;  // two half steps of bf16, and in size alone: the errors of D terms differ in sign
 
 struct BwdArgs {
     int P;           // positions per head (tiled mode: of the padded grid)
@@ -48,6 +55,7 @@ struct BwdArgs {
     float scale, scale_log2;
     const float *nlse, *ndelta;  // [BH, Pw]: -lse log2e (-inf: the row has no gradient) and -delta
     float *ndelta_out;           // dQ pass: ndelta with the row sums of dX taken off (see below)
+    const float *slack;          // [BH, Pw]: the most that a row's sum of dX can be of delta's error (see above)
     const float *none;           // 128 values of -inf, then 128 of 0: the statistics of columns past a list's end
     const float *kmean;          // mean key of each block (window mode: tile of 128), [BH, nt, D], or nullptr (see backward_dq.cu)
     const uint32_t *valid;       // [BH, Pw/32] bits: which positions hold a token; nullptr when all do
@@ -175,7 +183,7 @@ __device__ __forceinline__ void bwd_zero_row(void *out, int out_f32, size_t at, 
     for (int e = 0; e < n; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// dQ (and dbias) of every query block; dK and dV of every key block.  `kind`
+// dQ of every query block; dK, dV and the bias's partial sums of every key block.  `kind`
 // of kernel: block is 32, 64 or 128; window and bias need 128.
 vsa_status launch_bwd_dq(const BwdMaps &maps, const BwdArgs &a, int D, int block, bool window, bool tiled, bool bias,
                          cudaStream_t st);

@@ -459,8 +459,11 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         const float mine = row_sum[0] + row_sum[1];
         if (hf == 1) sSum[row] = mine;
         named_barrier(1, 256);
-        if (hf == 0 && ok && n > 0 && row < BS && nl != -INFINITY)
-            a.ndelta_out[static_cast<size_t>(bh) * a.Pw + p] = nd - (mine + sSum[row]);
+        if (hf == 0 && ok && n > 0 && row < BS && nl != -INFINITY) {
+            const float sum = mine + sSum[row];
+            if (fabsf(sum) <= chain_load(a.slack + static_cast<size_t>(bh) * a.Pw + p))
+                a.ndelta_out[static_cast<size_t>(bh) * a.Pw + p] = nd - sum;
+        }
 
         // ---- epilogue: warps 0-3 write the first half of the columns, 4-7 the second ----
         const int r = rows_live && row < BS && head_ok ? bwd_row_of<TILED>(p, a, tc) : -1;
@@ -474,10 +477,11 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         }
         // CENTER: sums and weighted means of the two halves of the columns meet in
         // the K ring, which nothing reads or fills any more
-        float *sUsed = reinterpret_cast<float *>(sK), *sMean = sUsed + 256;  // [2][128], [8][D + 1]
+        float *sUsed = reinterpret_cast<float *>(sK), *sAll = sUsed + 256, *sMean = sAll + 256;  // [2][128] twice, [8][D + 1]
         if constexpr (CENTER) {
             if (have) {
                 sUsed[hf * 128 + row] = used_sum[0] + used_sum[1];
+                sAll[hf * 128 + row] = mine;
                 #pragma unroll
                 for (int e = 0; e < CPL; ++e) sMean[warp * (D + 1) + CPL * lane + e] = center[e];
                 if (lane == 0) sMean[warp * (D + 1) + D] = mass;
@@ -495,6 +499,10 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                     const float total = c0[D] + c1[D];
                     inv = total > 0.f ? 1.f / total : 0.f;
                     used = sUsed[row] + sUsed[128 + row];
+                    // part of a softmax over more keys: what dX lost in rounding alone
+                    const float sum = sAll[row] + sAll[128 + row];
+                    if (row < BS && p < a.Pw && !(fabsf(sum) <= chain_load(a.slack + static_cast<size_t>(bh) * a.Pw + p)))
+                        used -= sum;
                 }
                 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {

@@ -487,7 +487,10 @@ vsa_status vsa_head_profile(const void *q, const void *k, int B, int n_heads, in
  * that is computed has weight zero, and zero times a non-finite q, k, v or
  * dout of that block is NaN; blocks that no list names are not read.
  *   dout       [B, n_heads, S, D] bf16, in the order of o
- *   o, o_lo, lse as the forward call wrote them, o in o_dtype; o_lo or NULL
+ *   o, o_lo, lse as the forward call wrote them, o in o_dtype; o_lo or NULL.
+ *              Or those of a softmax over more keys, joined from calls over
+ *              parts of them: the call then gives its own keys' part of dq
+ *              (the parts add up), and dk and dv of its keys
  *   dq, dk, dv [B, n_heads, S, D] in grad_dtype, in the order of q, k and v
  *   workspace  DEVICE scratch of the _workspace_size call's bytes, 256-byte
  *              aligned, one per call in flight

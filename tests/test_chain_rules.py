@@ -44,7 +44,7 @@ def test_tensor_memory_is_held_before_the_next_kernel_is_released(file, name, bo
 
 
 # what the kernels of a chain hand to one another, by the names that the readers use
-HANDED_ON = r"nlse|ndelta|valid|km|kmean|off|offsets|bits|part|tab|bm|t_off|t_rows"
+HANDED_ON = r"nlse|ndelta|slack|valid|km|kmean|off|offsets|bits|part|tab|bm|t_off|t_rows"
 
 
 @pytest.mark.parametrize("file", ["attention_pp.cu", "backward.cu", "backward_dkv.cu", "backward_dq.cu",

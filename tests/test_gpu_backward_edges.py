@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import block_sparse_self_b200 as vsa
-from test_gpu_backward import DEV, U, bucket_of, check, inputs, reference, window_mask
+from test_gpu_backward import DEV, U, bucket_of, check, inputs, list_mask, reference, window_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +226,57 @@ def test_bucket_borders_next_to_whole_numbers(buckets, far, border):
         if d <= far:
             assert int(got[far - d]) == bucket_of(d, buckets, far)
             assert int(got[far + d]) == buckets // 2 + bucket_of(d, buckets, far)
+
+
+# --------------------------------------------------------------------------
+# joined parts
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("mode,block,nb,D", [("short lists", 128, 6, 64), ("short lists", 32, 14, 128),
+                                             ("long lists", 32, 40, 64), ("long lists", 64, 24, 128),
+                                             ("window and lists", 128, 5, 64)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_gradients_of_joined_parts(mode, block, nb, D, out):
+    """A softmax over two sets of keys, each by a call of its own: every part's gradients from the joined o and lse.
+
+    A part's sum of dX is no error.  Only where it is at most 2u sum_d |g_d o_d| = 2u G_i may it be taken for one; the
+    bounds of dX grow by P_ij 2u G_i for that, and where dq is centered its own by scale 2u G_i max |k|.  Joining in
+    fp32 adds nothing to the half step of a bf16 o that the bounds have."""
+    H, S = 2, block * nb
+    q, k, v, g = inputs(1, H, S, D, seed=60 + S + D)
+    b = torch.arange(nb)
+    if mode == "window and lists":      # the window reaches 30 positions, the lists two blocks on
+        parts = [("window", (60, 0)), ("lists", [[(i + 2) % nb] for i in range(nb)])]
+    else:
+        n = 3 if mode == "short lists" else nb // 2
+        parts = [("lists", [sorted((i * 5 + s + 2 * e) % nb for e in range(n)) for i in range(nb)]) for s in (0, 1)]
+    see, res = torch.zeros(S, S, dtype=torch.bool, device=DEV), []
+    for kind, what in parts:
+        if kind == "window":
+            fwd, bwd, args = vsa.window_attention, vsa.window_attention_backward, what
+            mine = window_mask(S, *what)
+        else:
+            idx = torch.tensor(what, dtype=torch.int32, device=DEV)
+            cnt = torch.full((nb,), idx.shape[1], dtype=torch.int32, device=DEV)
+            fwd, bwd, args = vsa.block_sparse_attention, vsa.block_sparse_attention_backward, (idx, cnt, block)
+            mine = list_mask(idx, cnt, block, S)
+        assert not (see & mine).any()
+        see |= mine
+        res.append((*fwd(q, k, v, *args, out_dtype=torch.float32, return_lse=True), bwd, args))
+    lse = torch.logaddexp(res[0][1], res[1][1])
+    o = sum(x[0] * (x[1] - lse).exp()[..., None] for x in res).to(out)
+    dq, dk, dv = (sum(x) for x in zip(*(bwd(g, q, k, v, o, lse, *args, grad_dtype=torch.float32)
+                                        for _, _, bwd, args in res)))
+    scale = 1 / math.sqrt(D)
+    for h in range(H):
+        ref = reference(q[0, h], k[0, h], v[0, h], g[0, h], see)
+        q64, k64, v64, g64 = (x[0, h].double() for x in (q, k, v, g))
+        P = torch.exp((scale * q64 @ k64.T).masked_fill(~see, -math.inf) - ref["lse"][:, None])
+        G = 2 * U * (g64.abs() * ref["o"].abs()).sum(1, keepdim=True)
+        extra = P * G
+        bounds = dict(dq=ref["e_dq"] + scale * (extra @ k64.abs() + 2 * G * k64.abs().max()),
+                      dk=ref["e_dk"] + scale * extra.T @ q64.abs(), dv=ref["e_dv"])
+        for name, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+            off = (x[0, h].double() - ref[name]).abs()
+            assert (off <= bounds[name] + 1e-5).all(), name
+            assert off.norm() <= 0.02 * ref[name].norm(), name     # what is missing otherwise is of its own size
