@@ -188,11 +188,6 @@ struct Layout {
     size_t nlse, ndelta, slack, none, valid, kmean, t_off, t_rows, bits, part, bias, total;
 };
 
-// Whether dQ's rows are centered (backward_dq.cu says what it costs and brings):
-// windows always, lists where they hold at most 8 blocks.
-constexpr int kCenterBlocks = 8;
-bool centered(int lists, int cap) { return lists == 0 || cap <= kCenterBlocks; }
-
 Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, int buckets, int far) {
     const size_t Pw = (static_cast<size_t>(positions) + 127) / 128 * 128;
     Layout L{};
@@ -207,7 +202,7 @@ Layout layout(int BH, int H, int positions, int S, int lists, int nb, int cap, i
     L.slack = take(BH * Pw * 4);
     L.none = take(256 * 4);
     L.valid = take(BH * (Pw / 32) * 4);
-    if (centered(lists, cap)) L.kmean = take(BH * (lists > 0 ? nb : Pw / 128) * 128 * 4);  // D <= 128
+    L.kmean = take(BH * (lists > 0 ? nb : Pw / 128) * 128 * 4);  // D <= 128
     if (lists > 0) {
         L.t_off = take(static_cast<size_t>(lists) * (nb + 1) * 4);
         L.t_rows = take(static_cast<size_t>(lists) * nb * cap * 4);
@@ -322,7 +317,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
         a.buckets = buckets;
         a.dbias_part = B.dbias ? f32_at(lay.part) : nullptr;
     }
-    if (centered(lists, L.cap)) {
+    {
         float *kmean = f32_at(lay.kmean);
         auto means = L.D == 128 ? (L.block == 128 ? block_means_kernel<128, 128> : L.block == 64 ? block_means_kernel<128, 64> : block_means_kernel<128, 32>)
                                 : (L.block == 128 ? block_means_kernel<64, 128> : L.block == 64 ? block_means_kernel<64, 64> : block_means_kernel<64, 32>);
@@ -335,7 +330,7 @@ vsa_status launch_backward(const BackwardLaunch &B, void *workspace, int *status
     const dim3 grid((a.Pw / 32 + 7) / 8, L.BH);
     auto row_stats = L.D == 128 ? (B.o_f32 ? row_stats_kernel<128, true> : row_stats_kernel<128, false>)
                                 : (B.o_f32 ? row_stats_kernel<64, true> : row_stats_kernel<64, false>);
-    vsa_status r = check_cuda(launch_kernel(a.kmean != nullptr, row_stats, grid, dim3(256), 0, st, s),
+    vsa_status r = check_cuda(launch_kernel(true, row_stats, grid, dim3(256), 0, st, s),
                               "attention backward launch (row statistics)");
     if (r != VSA_OK) return r;
     if (lists > 0) {

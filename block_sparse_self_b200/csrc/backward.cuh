@@ -57,7 +57,7 @@ struct BwdArgs {
     float *ndelta_out;           // dQ pass: ndelta with the row sums of dX taken off (see below)
     const float *slack;          // [BH, Pw]: the most that a row's sum of dX can be of delta's error (see above)
     const float *none;           // 128 values of -inf, then 128 of 0: the statistics of columns past a list's end
-    const float *kmean;          // mean key of each block (window mode: tile of 128), [BH, nt, D], or nullptr (see backward_dq.cu)
+    const float *kmean;          // mean key of each block (window mode: tile of 128), [BH, nt, D] (see backward_dq.cu)
     const uint32_t *valid;       // [BH, Pw/32] bits: which positions hold a token; nullptr when all do
     void *d0, *d1;               // dQ pass: dq; dK/dV pass: dk, dv
     int out_f32;

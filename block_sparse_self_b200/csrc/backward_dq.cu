@@ -12,19 +12,24 @@
 // from, so the next tile's S is computed while this one is worked on, and dP
 // is refilled as soon as it has been read.
 //
-// Windows and short lists (CENTER): the keys that a row sees often have a mean far
-// larger than their spread (neighbouring positions are alike), and then dQ, which
-// only depends on the spread since sum_j dX_ij = 0, drowns in that mean times the
-// errors of dX.  So the row's sum of dX as the MMA got it, times a vector close to
-// its mean key, is taken off again at the end:
+// Centering: the keys that a row sees often have a mean far larger than their spread
+// (neighbouring positions are alike, a projection has a bias), and then dQ, which only
+// depends on the spread since sum_j dX_ij = 0, drowns in that mean times the errors of
+// dX.  So the row's sum of dX as the MMA got it, times a vector close to its mean key,
+// is taken off again at the end:
 //   dQ_i = scale (sum_j dX_ij k_j - (sum_j dX_ij) c),
-// an identity for any c.  c is, per 32 rows, the mean key of every block (windows:
-// tile of 128) weighted with the mass of P in it (from a quarter of the columns).
-// With it dQ's error against 64 bits falls from 4.1e-3 to 2.6e-3 of its norm (window
-// 4096, S = 16384), from 4.6e-3 to 2.6e-3 (window 159, S = 2048; 1.7e-3 is the rounding
-// to bf16), from 4.8e-3 to 3.0e-3 (3 of 1080 blocks of 32, o in bf16 without its remainder).
-// Longer lists average over the whole grid: 14 of 120 blocks of 64 go from 3.50e-3
-// to 3.43e-3 and would pay 228 -> 253 us for it, so lists of more than 8 go without.
+// an identity for any c.
+//  - Lists: c is the mean of the listed blocks' mean keys.  Keys with a mean of 0, 1, 4 and
+//    16 times their spread, lists of 12 of 40 blocks of 128: dQ's error against 64 bits is
+//    2.4e-3 of its norm for each, without it 2.4, 3.5, 10.5 and 39e-3 (1.7e-3 is the rounding
+//    to bf16).  The one sum also corrects delta; a sum of unrounded dX beside it would leave
+//    dK at 2.34e-3 in place of 2.45e-3 and take another 2 % of the training step.  With
+//    the blocks weighted by their mass of P, as for windows, dQ's error was 3.5 against
+//    3.6e-3 for lists of 3 of 1080 blocks of 32, and equal from 5 blocks of 64 on.
+//  - Windows: c is, per 32 rows, the mean key of every tile of 128 weighted with the mass
+//    of P in it (from a quarter of the columns): a wide window's plain mean is far from
+//    the keys at its middle.  4.1e-3 -> 2.6e-3 (window 4096, S = 16384), 4.6e-3 -> 2.6e-3
+//    (window 159, S = 2048).
 #include "backward.cuh"
 
 namespace vsa {
@@ -53,8 +58,7 @@ struct KeyWalk {
     }
 };
 
-// CENTER: the rows' sums of dX are taken off (see above).
-template <int D, int BS, bool WINDOW, bool TILED, bool BIAS, bool CENTER>
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, const __grid_constant__ BwdArgs a) {
     using C = DqCfg<D>;
@@ -290,13 +294,19 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
             nl = chain_load(a.nlse + static_cast<size_t>(bh) * a.Pw + p);
             nd = chain_load(a.ndelta + static_cast<size_t>(bh) * a.Pw + p);
         }
-        float row_sum[2] = {0.f, 0.f};
-        // CENTER: the row's sum of dX as rounded, the mass of P in this warp's
-        // columns, and sum over the blocks of mass times mean key (columns CPL lane ..)
+        // the row's sum of dX, unrounded and as rounded; windows: the mass of P in this
+        // warp's columns; sum of mean keys, in windows times their mass (columns CPL lane ..)
         constexpr int CPL = D / 32;
-        [[maybe_unused]] float used_sum[2] = {0.f, 0.f}, mass = 0.f, center[CPL];
+        [[maybe_unused]] float row_sum[2] = {0.f, 0.f}, mass = 0.f;
+        float used_sum[2] = {0.f, 0.f}, center[CPL];
         #pragma unroll
         for (int e = 0; e < CPL; ++e) center[e] = 0.f;
+        // += f times the mean key of the x-th listed block
+        auto add_mean = [&](int x, float f, float (&to)[CPL]) {
+            const float *km = a.kmean + (static_cast<size_t>(bh) * a.nt + w.at(x)) * D + CPL * lane;
+            #pragma unroll
+            for (int e = 0; e < CPL; ++e) to[e] = fmaf(f, chain_load(km + e), to[e]);
+        };
         // buckets of a key tile's three runs of 32 offsets (this lane's of each)
         [[maybe_unused]] int bk[3] = {0, 0, 0};
         [[maybe_unused]] auto fetch_buckets = [&](int j) {
@@ -306,6 +316,11 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         };
         if constexpr (BIAS) {
             if (n > 0) fetch_buckets(0);
+        }
+        if constexpr (!WINDOW) {
+            // every eighth listed block per warp, before the first scores are there
+            #pragma unroll 4
+            for (int x = warp; x < w.count; x += 8) add_mean(x, 1.f, center);
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -345,21 +360,11 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                     }
                 }
             }
+            [[maybe_unused]] float mean[CPL] = {};
+            if constexpr (WINDOW) add_mean(j, 1.f, mean);
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
             float pr[64];
-            // blocks in this warp's 64 columns (of blocks of 128, half of one)
-            constexpr int NB = BS < 64 ? 64 / BS : 1;
-            [[maybe_unused]] float mean[NB][CPL];
-            if constexpr (CENTER) {
-                #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const int x = WINDOW ? j : min(j * NSUB + 64 * hf / BS + b, w.count - 1);
-                    const float *km = a.kmean + (static_cast<size_t>(bh) * a.nt + w.at(x)) * D + CPL * lane;
-                    #pragma unroll
-                    for (int e = 0; e < CPL; ++e) mean[b][e] = chain_load(km + e);
-                }
-            }
             {
                 uint32_t x[64];
                 tmem_ld32(t_lane + (j & 1) * 128 + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
@@ -407,19 +412,16 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                 #pragma unroll
                 for (int c = 0; c < 64; ++c) pr[c] = ex2_approx(__uint_as_float(x[c]));
             }
-            if constexpr (CENTER) {
+            if constexpr (WINDOW) {
+                float m = 0.f;
                 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float m = 0.f;
-                    #pragma unroll
-                    for (int c = 64 / NB * b; c < 64 / NB * (b + 1); c += 4) m += pr[c];
-                    m = m < 1e30f ? m : 0.f;  // a row that is not finite must not reach its neighbours
-                    #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-                    mass += m;
-                    #pragma unroll
-                    for (int e = 0; e < CPL; ++e) center[e] = fmaf(m, mean[b][e], center[e]);
-                }
+                for (int c = 0; c < 64; c += 4) m += pr[c];
+                m = m < 1e30f ? m : 0.f;  // a row that is not finite must not reach its neighbours
+                #pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+                mass += m;
+                #pragma unroll
+                for (int e = 0; e < CPL; ++e) center[e] = fmaf(m, mean[e], center[e]);
             }
             if (!__all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
@@ -437,10 +439,12 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                         f32x2_split(mul_f32x2(f32x2(d0, d1),
                                               add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), ndx2)),
                                     d0, d1);
-                        row_sum[0] += d0;
-                        row_sum[1] += d1;
+                        if constexpr (WINDOW) {
+                            row_sum[0] += d0;
+                            row_sum[1] += d1;
+                        }
                         const uint32_t pk = pack_bf16x2(d0, d1);  // bf16: the type of the MMA's operand
-                        if constexpr (CENTER) add_bf16x2_f32(pk, used_sum[0], used_sum[1]);
+                        add_bf16x2_f32(pk, used_sum[0], used_sum[1]);
                         dsk[16 * u + (c >> 1)] = pk;
                     }
                 }
@@ -456,7 +460,7 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
         }
         if (!ok && !*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
         // delta + the row's sum of dX, for the dK/dV pass (see backward.cuh)
-        const float mine = row_sum[0] + row_sum[1];
+        const float mine = WINDOW ? row_sum[0] + row_sum[1] : used_sum[0] + used_sum[1];
         if (hf == 1) sSum[row] = mine;
         named_barrier(1, 256);
         if (hf == 0 && ok && n > 0 && row < BS && nl != -INFINITY) {
@@ -475,16 +479,23 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
             have = false;
             if (!*abort_flag) { report(a.status, DEV_TIMEOUT); *abort_flag = 1; }
         }
-        // CENTER: sums and weighted means of the two halves of the columns meet in
+        // sums and mean keys of the two halves of the columns, or of all warps, meet in
         // the K ring, which nothing reads or fills any more
         float *sUsed = reinterpret_cast<float *>(sK), *sAll = sUsed + 256, *sMean = sAll + 256;  // [2][128] twice, [8][D + 1]
-        if constexpr (CENTER) {
-            if (have) {
-                sUsed[hf * 128 + row] = used_sum[0] + used_sum[1];
-                sAll[hf * 128 + row] = mine;
-                #pragma unroll
-                for (int e = 0; e < CPL; ++e) sMean[warp * (D + 1) + CPL * lane + e] = center[e];
-                if (lane == 0) sMean[warp * (D + 1) + D] = mass;
+        float *sEven = sMean + 8 * (D + 1);                                                       // [D]
+        if (have) {
+            sUsed[hf * 128 + row] = used_sum[0] + used_sum[1];
+            sAll[hf * 128 + row] = mine;
+            #pragma unroll
+            for (int e = 0; e < CPL; ++e) sMean[warp * (D + 1) + CPL * lane + e] = center[e];
+            if (lane == 0) sMean[warp * (D + 1) + D] = mass;
+        }
+        named_barrier(1, 256);
+        if constexpr (!WINDOW) {
+            if (have && threadIdx.x < D) {
+                float t = 0.f;
+                for (int x = 0; x < 8; ++x) t += sMean[x * (D + 1) + threadIdx.x];
+                sEven[threadIdx.x] = t / static_cast<float>(w.count);
             }
             named_barrier(1, 256);
         }
@@ -493,27 +504,27 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
                 tc_fence_after();
                 // the center first, then times the row's sum: a mass as small as fp32 has (all
                 // weight on columns that do not count for it) would take the sum to infinity
-                [[maybe_unused]] float used = 0.f, inv = 0.f;
+                [[maybe_unused]] float inv = 0.f;
                 [[maybe_unused]] const float *c0 = sMean + wq * (D + 1), *c1 = sMean + (wq + 4) * (D + 1);
-                if constexpr (CENTER) {
+                if constexpr (WINDOW) {
                     const float total = c0[D] + c1[D];
                     inv = total > 0.f ? 1.f / total : 0.f;
-                    used = sUsed[row] + sUsed[128 + row];
-                    // part of a softmax over more keys: what dX lost in rounding alone
-                    const float sum = sAll[row] + sAll[128 + row];
-                    if (row < BS && p < a.Pw && !(fabsf(sum) <= chain_load(a.slack + static_cast<size_t>(bh) * a.Pw + p)))
-                        used -= sum;
                 }
+                float used = sUsed[row] + sUsed[128 + row];
+                // part of a softmax over more keys: what dX lost in rounding alone, if that is known
+                const float sum = sAll[row] + sAll[128 + row];
+                if (row < BS && p < a.Pw && !(fabsf(sum) <= chain_load(a.slack + static_cast<size_t>(bh) * a.Pw + p)))
+                    used -= sum;
                 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t x[32];
                     const int col = hf * (D / 2) + 32 * c;
                     tmem_ld32(t_lane + C::DQ_COL + col, x);
                     tmem_ld_wait();
-                    if constexpr (CENTER) {
-                        #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            x[e] = __float_as_uint(fmaf(-used, (c0[col + e] + c1[col + e]) * inv, __uint_as_float(x[e])));
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float c = !WINDOW ? sEven[col + e] : (c0[col + e] + c1[col + e]) * inv;
+                        x[e] = __float_as_uint(fmaf(-used, c, __uint_as_float(x[e])));
                     }
                     if (r >= 0) bwd_store32(x, a.scale, a.d0, a.out_f32, at + col);
                 }
@@ -531,10 +542,10 @@ bwd_dq_kernel(const __grid_constant__ BwdMapsOf<TILED ? kMaxTiles : 1> maps, con
     }
 }
 
-template <int D, int BS, bool WINDOW, bool TILED, bool BIAS, bool CENTER>
+template <int D, int BS, bool WINDOW, bool TILED, bool BIAS>
 vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
     using C = DqCfg<D>;
-    auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS, CENTER>;
+    auto kern = bwd_dq_kernel<D, BS, WINDOW, TILED, BIAS>;
     constexpr int smem = C::SMEM + (BIAS ? kMaxBuckets * 4 : 0);
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -543,19 +554,18 @@ vsa_status run(const BwdMaps &maps, const BwdArgs &a, cudaStream_t st) {
                       "attention backward launch (dQ)");
 }
 
-template <int D, bool TILED, bool CENTER>
+template <int D, bool TILED>
 vsa_status pick_lists(const BwdMaps &maps, const BwdArgs &a, int block, cudaStream_t st) {
-    if (block == 128) return run<D, 128, false, TILED, false, CENTER>(maps, a, st);
-    return block == 64 ? run<D, 64, false, TILED, false, CENTER>(maps, a, st)
-                       : run<D, 32, false, TILED, false, CENTER>(maps, a, st);
+    if (block == 128) return run<D, 128, false, TILED, false>(maps, a, st);
+    return block == 64 ? run<D, 64, false, TILED, false>(maps, a, st)
+                       : run<D, 32, false, TILED, false>(maps, a, st);
 }
 
 template <int D>
 vsa_status pick(const BwdMaps &maps, const BwdArgs &a, int block, bool window, bool tiled, bool bias, cudaStream_t st) {
     if (window)
-        return bias ? run<D, 128, true, false, true, true>(maps, a, st) : run<D, 128, true, false, false, true>(maps, a, st);
-    if (a.kmean) return tiled ? pick_lists<D, true, true>(maps, a, block, st) : pick_lists<D, false, true>(maps, a, block, st);
-    return tiled ? pick_lists<D, true, false>(maps, a, block, st) : pick_lists<D, false, false>(maps, a, block, st);
+        return bias ? run<D, 128, true, false, true>(maps, a, st) : run<D, 128, true, false, false>(maps, a, st);
+    return tiled ? pick_lists<D, true>(maps, a, block, st) : pick_lists<D, false>(maps, a, block, st);
 }
 
 }  // namespace

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import block_sparse_self_b200 as vsa
-from test_gpu_backward import DEV, U, bucket_of, check, inputs, list_mask, reference, window_mask
+from test_gpu_backward import (DEV, U, bucket_of, check, inputs, list_mask, order_of, random_lists, reference,
+                               window_mask)
 
 pytestmark = pytest.mark.gpu
 
@@ -51,6 +52,79 @@ def test_center_of_a_vanishing_mass(mode):
     mass = 16 * math.exp(-86)
     assert (ref["e_dX"].sum(1) / mass).max() > torch.finfo(torch.float32).max
     check([x[0, 0] for x in got], ref)
+
+
+def check_centered(dq, q, k, v, g, see):
+    """dq against what independent roundings add up to where they multiply k - c, c the mean of the keys a row sees:
+    var dq_i = scale^2 (u^2/3 sum_j dX_ij^2 (k_j - c)^2 + var delta_i (sum_j P_ij (k_j - c))^2), the two terms of
+    test_gpu_backward.py, and for the sums that are taken off n roundings to fp32 of size |c| |dX|.  Five times that;
+    with c = 0 (keys 16 times as far from zero as from one another) it would be 16 times."""
+    ref = reference(q, k, v, g, see)
+    k64, n = k.double(), see.sum(1, keepdim=True)
+    scale = 1 / math.sqrt(q.shape[1])
+    c = see.double() @ k64 / n
+    P = torch.exp((scale * q.double() @ k64.T).masked_fill(~see, -math.inf) - ref["lse"][:, None])
+    dX2 = ref["dX"] ** 2
+    spread = (dX2 @ k64 ** 2 - 2 * c * (dX2 @ k64) + c ** 2 * dX2.sum(1, keepdim=True)).clamp(min=0)
+    h2 = U * U / 3
+    var_o = h2 * (ref["o"] ** 2 + P ** 2 @ v.double() ** 2 - 2 * ref["o"] * (P ** 2 @ v.double())
+                  + ref["o"] ** 2 * (P ** 2).sum(1, keepdim=True))
+    var_delta = (g.double() ** 2 * var_o).sum(1, keepdim=True)
+    var = scale ** 2 * (h2 * spread + var_delta * (P @ k64 - c) ** 2 + n * 2.0 ** -48 * c ** 2 * dX2.sum(1, keepdim=True))
+    assert (dq.double() - ref["dq"]).norm() <= 5 * var.sum().sqrt()
+
+
+def far_keys(H, S, D):
+    q, k, v, g = inputs(1, H, S, D, seed=S + D)
+    m = torch.randn(1, H, 1, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    return (q.float() / 16).bfloat16(), (k.float() + 16 * m).bfloat16(), v, g
+
+
+@pytest.mark.parametrize("block,nb,D,longest", [(128, 20, 128, 12), (64, 30, 64, 14), (32, 60, 128, 40), (128, 9, 64, 9),
+                                                (128, 8, 64, 3)])
+def test_lists_gradients_of_keys_with_a_large_mean(block, nb, D, longest):
+    """dq's errors multiply the keys' spread and not their mean, however many blocks are listed."""
+    H = 2
+    q, k, v, g = far_keys(H, block * nb, D)
+    idx, cnt = random_lists(1, H, nb, longest, seed=nb)
+    o, lse, o_lo = vsa.block_sparse_attention(q, k, v, idx, cnt, block, return_remainder=True)
+    dq = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block, grad_dtype=torch.float32, o_lo=o_lo)[0]
+    for h in range(H):
+        check_centered(dq[0, h], q[0, h], k[0, h], v[0, h], g[0, h], list_mask(idx[0, h], cnt[0, h], block, block * nb))
+
+
+def test_sliding_tile_gradients_of_keys_with_a_large_mean():
+    grid, H, D = (8, 16, 24), 2, 64
+    S = math.prod(grid)
+    q, k, v, g = far_keys(H, S, D)
+    tok = order_of(grid, (4, 8, 8), grid).to(DEV)
+    idx, cnt, group = vsa.structured_block_list("sliding_tile", grid)
+    assert group == 0 and int(cnt.max()) > 8
+    at = torch.empty(S, dtype=torch.long, device=DEV)
+    at[tok] = torch.arange(S, device=DEV)
+    see = list_mask(idx, cnt, 128, S)[at][:, at]
+    args = (grid, [(4, 8, 8)], None, idx, cnt)
+    o, lse, o_lo = vsa.block_sparse_attention_tiled(q, k, v, *args, return_remainder=True)
+    dq = vsa.block_sparse_attention_tiled_backward(g, q, k, v, o, lse, *args, grad_dtype=torch.float32, o_lo=o_lo)[0]
+    for h in range(H):
+        check_centered(dq[0, h], q[0, h], k[0, h], v[0, h], g[0, h], see)
+
+
+@pytest.mark.parametrize("block", [32, 64, 128])
+def test_the_room_of_a_list_changes_nothing(block):
+    """The same lists in wider rows: the same bits, forward and backward."""
+    nb, D = 12, 64
+    q, k, v, g = inputs(1, 2, block * nb, D, seed=block)
+    idx, cnt = random_lists(1, 2, nb, 4, seed=block)
+    res = []
+    for cap in (4, 8, 9, 12):
+        wide = torch.full((1, 2, nb, cap), -1, dtype=torch.int32, device=DEV)
+        wide[..., :4] = idx
+        o, lse, o_lo = vsa.block_sparse_attention(q, k, v, wide, cnt, block, return_remainder=True)
+        res.append((o, lse, o_lo, *vsa.block_sparse_attention_backward(g, q, k, v, o, lse, wide, cnt, block, o_lo=o_lo)))
+    for other in res[1:]:
+        for x, y in zip(res[0], other):
+            assert torch.equal(x, y)
 
 
 # --------------------------------------------------------------------------
