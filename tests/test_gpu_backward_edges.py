@@ -354,3 +354,49 @@ def test_gradients_of_joined_parts(mode, block, nb, D, out):
             off = (x[0, h].double() - ref[name]).abs()
             assert (off <= bounds[name] + 1e-5).all(), name
             assert off.norm() <= 0.02 * ref[name].norm(), name     # what is missing otherwise is of its own size
+
+
+# --------------------------------------------------------------------------
+# groups that are not a power of two and cross blocks; blocks of 32 and 64 under structured masks
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("block,nb,D,group", [(128, 4, 64, 96), (128, 5, 128, 100), (128, 3, 64, 200), (64, 7, 128, 48),
+                                              (64, 6, 64, 130), (32, 13, 64, 24), (32, 9, 128, 37)])
+def test_groups_that_cross_blocks(block, nb, D, group):
+    """A row's group of keys lies in one listed block or in several; the last group is cut by the end."""
+    H, S = 2, block * nb
+    q, k, v, g = inputs(1, H, S, D, seed=S + group)
+    i = torch.arange(nb)
+    lo, hi = i * block // group * group // block, ((i * block + block - 1) // group * group + group - 1) // block
+    lists = [list(range(int(a), min(int(b), nb - 1) + 1)) for a, b in zip(lo, hi)]
+    lists[-1] = sorted({0, *lists[-1]})     # a block that none of its rows sees a key of
+    cap = max(map(len, lists))
+    idx = torch.tensor([x + [-1] * (cap - len(x)) for x in lists], dtype=torch.int32, device=DEV)
+    cnt = torch.tensor([len(x) for x in lists], dtype=torch.int32, device=DEV)
+    p = torch.arange(S, device=DEV) // group
+    see = list_mask(idx, cnt, block, S) & (p[:, None] == p)
+    assert (see == (p[:, None] == p)).all()
+    o, lse = vsa.block_sparse_attention(q, k, v, idx, cnt, block, group, return_lse=True)
+    got = vsa.block_sparse_attention_backward(g, q, k, v, o, lse, idx, cnt, block, group, grad_dtype=torch.float32)
+    for h in range(H):
+        ref = reference(q[0, h], k[0, h], v[0, h], g[0, h], see)
+        assert ((o[0, h].double() - ref["o"]).abs() <= ref["e_o"] + 1e-6).all()
+        check([x[0, h] for x in got], ref, what=f"head {h}")
+
+
+@pytest.mark.parametrize("kind,grid,block", [("spatial", (3, 8, 12), 32), ("temporal", (16, 4, 8), 64), ("temporal", (8, 4, 8), 32),
+                                             ("spatial", (6, 4, 8), 64), ("temporal", (64, 2, 4), 32)])
+def test_structured_masks_of_short_blocks(kind, grid, block):
+    """The path of permuted tensors and groups, differentiated through."""
+    D, H = 64, 2
+    S = math.prod(grid)
+    q, k, v, g = inputs(1, H, S, D, seed=S + block)
+    plain = vsa.structured_attention(q, k, v, kind, grid, block)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    o = vsa.structured_attention(*leaves, kind, grid, block)
+    assert (o - plain).abs().max() <= 4 * U * v.abs().max()     # another kernel's rounding
+    got = torch.autograd.grad(o, leaves, g)
+    i = torch.arange(S, device=DEV)
+    label = i // (grid[1] * grid[2]) if kind == "spatial" else i % (grid[1] * grid[2])
+    for h in range(H):
+        check([x[0, h] for x in got], reference(q[0, h], k[0, h], v[0, h], g[0, h], label[:, None] == label))
