@@ -183,6 +183,14 @@ def padded_grid(grid, tiles) -> Tuple[int, int, int]:
     return (out.t, out.h, out.w)
 
 
+def _padded_tokens(grid, tiles) -> int:
+    """_grid_tokens(padded_grid(grid, tiles)) without a library call: a quarter of its time, in every tiled call."""
+    steps = [math.lcm(*(int(t[a]) for t in tiles)) for a in range(3)] if tiles else [0]
+    if min(steps) <= 0:
+        return _grid_tokens(padded_grid(grid, tiles))  # which says what is wrong with them
+    return math.prod(-(-int(g) // s) * s for g, s in zip(grid, steps))
+
+
 def _grid_tokens(grid) -> int:
     return int(grid[0]) * int(grid[1]) * int(grid[2])
 
@@ -516,7 +524,7 @@ def _check_block_lists(idx, cnt, B, H, S, block):
 
 def _check_tiled_lists(idx, cnt, B, H, grid, tiles):
     """_check_lists for blocks of the padded grid; the number of its positions, and the block."""
-    positions, volume = _grid_tokens(padded_grid(grid, tiles)), math.prod(int(x) for x in tiles[0])
+    positions, volume = _padded_tokens(grid, tiles), math.prod(int(x) for x in tiles[0])
     block = min(128, volume)
     if volume not in (32, 64) and volume % 128:
         raise ValueError(f"the tile volume must be 32, 64 or a multiple of 128, got {volume}")

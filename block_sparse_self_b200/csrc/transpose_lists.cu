@@ -10,8 +10,10 @@
 // A list of up to 128 blocks is turned by one CTA in shared memory: one launch,
 // no workspace.  Longer ones go through global memory in three kernels, spread
 // over the SMs.  What bounds both is latency (launches, then the lists' rows),
-// not bytes: 7 blocks take 4.4 us against 9.8, 120 blocks 11.5 against 16, but
-// 240 blocks 22 against 17 and 960 blocks 80 against 32 (kernel times).
+// not bytes.  24 lists, one CTA each against three kernels: 7 blocks 3.6 us against
+// 5.0, 64 blocks 5.9 against 7.6, 120 blocks 9.0 against 8.6, 160 blocks 10.8 against
+// 9.1, 240 blocks 17.3 against 8.9, 960 blocks 66.7 against 19.4 (launches in a row
+// in a graph; called one by one three launches take the host 19.5 us and one 13.4).
 #include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"

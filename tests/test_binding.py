@@ -233,3 +233,14 @@ def test_training_calls_launch_with_their_tensors_device_current(host, monkeypat
     forward = len(launched)
     o.sum().backward()
     assert forward >= 1 and len(launched) > forward
+
+
+def test_tokens_of_the_padded_grid():
+    for grid, tiles in (((16, 45, 80), [(1, 8, 16), (2, 8, 8), (4, 4, 8)]), ((3, 7, 20), [(1, 8, 16)]),
+                        ((1, 1, 1), [(2, 4, 4), (1, 4, 8)]), ((4, 8, 16), [(1, 8, 16)])):
+        assert vsa._padded_tokens(grid, tiles) == math.prod(vsa.padded_grid(grid, tiles))
+    for tiles in ([], [(1, 0, 16)], [(0, 0, 0)]):
+        with pytest.raises(ValueError):
+            vsa._padded_tokens((4, 8, 16), tiles)
+        with pytest.raises(ValueError):
+            vsa._check_tiled_lists(*lists(1, 1, 4), 1, 1, (4, 8, 16), tiles)
