@@ -94,7 +94,7 @@ def test_lists_gradients_of_keys_with_a_large_mean(block, nb, D, longest):
 
 
 def test_sliding_tile_gradients_of_keys_with_a_large_mean():
-    grid, H, D = (8, 16, 24), 2, 64
+    grid, H, D = (4, 24, 24), 2, 64
     S = math.prod(grid)
     q, k, v, g = far_keys(H, S, D)
     tok = order_of(grid, (4, 8, 8), grid).to(DEV)
