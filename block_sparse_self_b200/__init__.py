@@ -864,8 +864,8 @@ def block_sparse_attention_tiled_backward(do, q, k, v, o, lse, grid, tiles, choi
                                           scale: Optional[float] = None, group_stride: int = 0, grad_dtype=None,
                                           o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of block_sparse_attention_tiled, all in T-major order, for the gradient `do` of its
-    output, from that output and its lse (and its remainder o_lo, if there is one).  The gradients
-    have q's type unless grad_dtype says otherwise."""
+    output, from that output and its lse (and its remainder o_lo, if there is one; or joined ones, as
+    for block_sparse_attention_backward).  The gradients have q's type unless grad_dtype says otherwise."""
     _qkv_shape(q, k, v)
     gdt = _out_dtype(grad_dtype, q)
     _check_saved(do, q, o, lse, o_lo)
@@ -988,7 +988,8 @@ def window_attention_backward(do, q, k, v, o, lse, window: int, sink: int = 0, s
                               bias: Optional[torch.Tensor] = None, max_distance: int = 128, grad_dtype=None,
                               bias_grad: bool = True, o_lo: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of window_attention for the gradient `do` of its output, from that output and its
-    lse (and its remainder o_lo, if there is one); with a bias (dq, dk, dv, dbias), dbias in the
+    lse (and its remainder o_lo, if there is one; or joined ones, as for
+    block_sparse_attention_backward); with a bias (dq, dk, dv, dbias), dbias in the
     bias's type, or None with bias_grad=False.  The gradients of q, k and v have q's type unless
     grad_dtype says otherwise."""
     _qkv_shape(q, k, v)
