@@ -561,7 +561,7 @@ attn_pp_kernel(const __grid_constant__ MapSet maps, const PPArgs a) {
             [[maybe_unused]] bool flat = true;
             if constexpr (BIAS) {
                 const int b0 = __shfl_sync(0xffffffffu, bk[4], 0);
-                flat = usual && __all_sync(0xffffffffu, bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
+                flat = __all_sync(0xffffffffu, usual && bk[0] == b0 && bk[1] == b0 && bk[2] == b0 && bk[3] == b0 && bk[4] == b0);
                 if (flat) add = sTab[b0];
                 else mul = 1.f;
             }
